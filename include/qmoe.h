@@ -88,17 +88,17 @@ typedef enum {
   QMOE_U8 = 2,
   QMOE_I32 = 3,
   QMOE_I64 = 4,
-  QMOE_F16 = 5,  /* GroupedMatMul only */
-  QMOE_BF16 = 6, /* GroupedMatMul only */
+  QMOE_F16 = 5,  /* GroupedMatMul, dispatch / combine and linear layers */
+  QMOE_BF16 = 6, /* GroupedMatMul, dispatch / combine and linear layers */
   QMOE_F64 = 7   /* GroupedMatMul only */
 } qmoe_dtype;
 
 typedef enum {
   QMOE_ACT_RELU = 0,
   QMOE_ACT_SWIGLU = 1,
-  QMOE_ACT_GELU = 2,     /* float MoE only */
-  QMOE_ACT_SILU = 3,     /* float MoE only */
-  QMOE_ACT_IDENTITY = 4  /* float MoE only */
+  QMOE_ACT_GELU = 2,     /* float MoE and linear layers */
+  QMOE_ACT_SILU = 3,     /* float MoE and linear layers */
+  QMOE_ACT_IDENTITY = 4  /* float MoE and linear layers */
 } qmoe_activation;
 
 typedef enum {
@@ -420,6 +420,164 @@ qmoe_status qmoe_moe_forward_debug(const qmoe_tensor* input, const qmoe_tensor* 
                                    const qmoe_moe_attrs* attrs, const qmoe_tensor* output,
                                    void* workspace, size_t workspace_bytes, void* stream,
                                    const qmoe_debug* debug);
+
+/* ------------------------------------------------------------------------
+ * The steps of a routed layer on their own, with their gradients: routing
+ * weights, tokens sorted by expert and back, and linear layers (dense, or one
+ * weight per expert over the sorted rows).  A training step of a routed layer
+ * is qmoe_route -> qmoe_dispatch -> qmoe_linear (FC1, activation) ->
+ * qmoe_linear (FC2) -> qmoe_combine, and the backward calls in reverse; a
+ * dense qmoe_linear with the combined rows as its residual adds a shared
+ * expert.  Row types: QMOE_F32, QMOE_F16 or QMOE_BF16, one type T per call;
+ * routing weights and router logits are float32.  Sums, softmax statistics
+ * and activations are float32; each result is rounded once to its type (to
+ * nearest, ties to even).  No result depends on the order of atomics: calls
+ * with equal arguments give equal bits.
+ * Conventions (ownership, streams, status, no allocation, one workspace per
+ * call in flight, capture in a HIP graph) as above; device pointers are
+ * aligned to their element unless stated; outputs must not alias inputs.
+ * Rank or extents that disagree: QMOE_ERR_SHAPE; other types than those
+ * named: QMOE_ERR_DTYPE.
+ * ------------------------------------------------------------------------ */
+
+/* Routing weights: indices [T, k] (int32) = the k largest logits of each row
+ * of router_probs [T, E], largest first, equal logits by ascending index;
+ * weights [T, k] = their softmax over the selection (QMOE_ROUTE_QMOE, or
+ * QMOE_ROUTE_MOE with normalize_routing_weights 1) or over all E logits
+ * (QMOE_ROUTE_MOE).  For finite logits the selection is qmoe_forward's.
+ * A logit of -infinity (or NaN) masks its expert: it is never selected; a row
+ * with fewer than k experts left fills up with index -1 and weight 0 (which
+ * qmoe_dispatch drops).  A logit of +infinity makes the row's weights NaN.
+ * 1 <= k <= E (QMOE_ERR_ATTR); E <= 1024, T * k < 2^30 (QMOE_ERR_UNSUPPORTED). */
+qmoe_status qmoe_route(const qmoe_tensor* router_probs, int32_t k, int32_t routing,
+                       int32_t normalize_routing_weights, const qmoe_tensor* indices, const qmoe_tensor* weights,
+                       void* stream);
+
+/* Gradient of qmoe_route at the logits: grad_router_probs [T, E] from
+ * grad_weights [T, k], with the forward's router_probs and indices (int32 or
+ * int64).  The selection itself is constant.  With w the weights and
+ * mean = sum_s w_s grad_weights_s: softmax over the selection,
+ * w_s (grad_weights_s - mean) at the selected experts and 0 elsewhere;
+ * softmax over all, ([e selected] grad_weights_e - mean) p_e everywhere.
+ * Masked experts get 0, as do slots with an index outside [0, E). */
+qmoe_status qmoe_route_backward(const qmoe_tensor* grad_weights, const qmoe_tensor* router_probs,
+                                const qmoe_tensor* indices, int32_t routing, int32_t normalize_routing_weights,
+                                const qmoe_tensor* grad_router_probs, void* stream);
+
+/* Tokens to experts: the T k slots (slot t k + s) are sorted by indices [T, k]
+ * (int32 or int64; expert 0 .. experts - 1), stable, and each slot's row of
+ * rows [T k, H] is a copy of its token's row of input [T, H].
+ *   offsets [experts + 1]  first row of each expert, then the first row behind
+ *                          the last
+ *   perm [T k] or NULL     slot of each row
+ *   inverse [T, k]         row of each slot
+ * (all int32).  A slot whose index lies outside [0, experts) is dropped: it
+ * takes a row behind the last expert's (in slot order), which is zero, and
+ * inverse holds -1 - row.  experts <= 1023, T * k < 2^30
+ * (QMOE_ERR_UNSUPPORTED).  workspace: qmoe_dispatch_workspace_size bytes,
+ * 256-byte aligned (NULL when 0: up to 4096 slots need none). */
+qmoe_status qmoe_dispatch_workspace_size(const qmoe_tensor* input, const qmoe_tensor* indices, int64_t experts,
+                                         size_t* bytes);
+qmoe_status qmoe_dispatch(const qmoe_tensor* input, const qmoe_tensor* indices, int64_t experts,
+                          const qmoe_tensor* rows, const qmoe_tensor* offsets, const qmoe_tensor* perm,
+                          const qmoe_tensor* inverse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradient of qmoe_dispatch at its input: grad_input [T, H] = the sum of the
+ * rows of grad_rows [T k, H] of each token's slots, in slot order (dropped
+ * slots: nothing; their rows are not read). */
+qmoe_status qmoe_dispatch_backward(const qmoe_tensor* grad_rows, const qmoe_tensor* inverse,
+                                   const qmoe_tensor* grad_input, void* stream);
+
+/* Rows back to tokens: output [T, H] = sum over a token's slots of
+ * weights [T, k] (float32; NULL: 1) times its row of rows [T k, H], in slot
+ * order.  inverse as qmoe_dispatch writes it; a slot whose inverse lies
+ * outside [0, T k) adds nothing and its row is not read. */
+qmoe_status qmoe_combine(const qmoe_tensor* rows, const qmoe_tensor* inverse, const qmoe_tensor* weights,
+                         const qmoe_tensor* output, void* stream);
+
+/* Gradients of qmoe_combine: grad_rows [T k, H] = weight times the token's row
+ * of grad_output [T, H], at the slot's row; grad_weights [T, k] (float32) =
+ * the dot product of both rows.  A dropped slot (inverse -1 - row) gets a zero
+ * row and weight gradient.  Either gradient may be NULL.  inverse must hold
+ * each row once (two slots of one row would both write it). */
+qmoe_status qmoe_combine_backward(const qmoe_tensor* grad_output, const qmoe_tensor* rows, const qmoe_tensor* inverse,
+                                  const qmoe_tensor* weights, const qmoe_tensor* grad_rows,
+                                  const qmoe_tensor* grad_weights, void* stream);
+
+/* Attributes of a linear layer, defaults in brackets. */
+typedef struct {
+  int32_t activation_type;   /* [IDENTITY] any qmoe_activation                    */
+  int32_t swiglu_fusion;     /* [0]  swiglu: 1 (interleaved gate / linear columns);
+                                     0 and 2 are QMOE_ERR_UNSUPPORTED with swiglu */
+  float activation_alpha;    /* [1]  swiglu gate sigmoid slope                    */
+  float activation_beta;     /* [0]  added to the swiglu linear branch            */
+  int32_t has_swiglu_limit;  /* [0]  1: swiglu_limit is given                     */
+  float swiglu_limit;        /* [-]  swiglu clamp L > 0, as for QMoE              */
+} qmoe_linear_attrs;
+
+/* Fill *a with the defaults listed above.  a must not be NULL. */
+void qmoe_linear_attrs_default(qmoe_linear_attrs* a);
+
+/* Linear layer with its epilogue:
+ *
+ *   preact = input weights^T + bias                              [M, N]
+ *   output = act(preact) (+ residual)                            [M, No]
+ *
+ * input [M, K]; weights [N, K], or [G, N, K] with offsets [G + 1] (int32, on
+ * the device): rows offsets[g] .. offsets[g + 1] - 1 of input take weight and
+ * bias g (qmoe_dispatch's rows and offsets).  bias [N] or [G, N], or NULL.
+ * act: relu, gelu h Phi(h), silu, identity (No = N), or swiglu over
+ * interleaved columns, g = preact[2j], u = preact[2j + 1] (No = N / 2, N even;
+ * the formula and limit of QMoE).  residual [M, No] is added after the
+ * activation, or NULL.  preact: NULL, or [M, N] to be kept for the backward
+ * pass (rounded to T; output is taken from the unrounded sums).  All of one
+ * type T.
+ * Rows behind the last group (from offsets[G] on) are zero in output and
+ * preact, their input and residual are not read.  offsets must not fall;
+ * offsets[0] is taken as 0.  Offsets outside [0, M] or falling make no access
+ * leave the tensors, but leave the results unspecified.
+ * Products: T float32, float32 matrix instructions; float16 and bfloat16,
+ * exact products of the 16-bit values summed in float32.  A long reduction
+ * over few rows is cut into ranges whose float32 sums are added in order.
+ * input and weights 16-byte aligned when K is a whole number of 16-byte runs
+ * (else they are first copied to padded rows in the workspace).
+ * G <= 1023, M <= 2^30, K and N <= 2^20 (QMOE_ERR_UNSUPPORTED).
+ * workspace: qmoe_linear_workspace_size bytes, 256-byte aligned (NULL when
+ * 0). */
+qmoe_status qmoe_linear_workspace_size(const qmoe_tensor* input, const qmoe_tensor* weights, const qmoe_tensor* bias,
+                                       const qmoe_tensor* residual, const qmoe_tensor* offsets,
+                                       const qmoe_linear_attrs* attrs, const qmoe_tensor* output,
+                                       const qmoe_tensor* preact, size_t* bytes);
+qmoe_status qmoe_linear(const qmoe_tensor* input, const qmoe_tensor* weights, const qmoe_tensor* bias,
+                        const qmoe_tensor* residual, const qmoe_tensor* offsets, const qmoe_linear_attrs* attrs,
+                        const qmoe_tensor* output, const qmoe_tensor* preact, void* workspace, size_t workspace_bytes,
+                        void* stream);
+
+/* Gradients of qmoe_linear from grad_output [M, No] (which is also the
+ * gradient at the residual):
+ *
+ *   d            = grad_output act'(preact)                      [M, N]
+ *   grad_input   = d weights                                     [M, K]
+ *   grad_weights = d^T input, per group                          [N, K] or [G, N, K]
+ *   grad_bias    = column sums of d, per group                   [N] or [G, N]
+ *
+ * Any of the three may be NULL.  preact as the forward kept it (NULL for the
+ * identity).  relu passes its gradient where preact > 0, a swiglu limit where
+ * the value is not beyond it.  For the 16-bit types d is rounded to T as the
+ * operand of the two products (grad_bias adds the unrounded d).  Rows behind
+ * the last group: zero in grad_input, nothing in the others; a group without
+ * rows gets zeros.  grad_output is 16-byte aligned for the identity with N a
+ * whole number of 16-byte runs; otherwise as qmoe_linear. */
+qmoe_status qmoe_linear_backward_workspace_size(const qmoe_tensor* grad_output, const qmoe_tensor* input,
+                                                const qmoe_tensor* weights, const qmoe_tensor* preact,
+                                                const qmoe_tensor* offsets, const qmoe_linear_attrs* attrs,
+                                                const qmoe_tensor* grad_input, const qmoe_tensor* grad_weights,
+                                                const qmoe_tensor* grad_bias, size_t* bytes);
+qmoe_status qmoe_linear_backward(const qmoe_tensor* grad_output, const qmoe_tensor* input, const qmoe_tensor* weights,
+                                 const qmoe_tensor* preact, const qmoe_tensor* offsets,
+                                 const qmoe_linear_attrs* attrs, const qmoe_tensor* grad_input,
+                                 const qmoe_tensor* grad_weights, const qmoe_tensor* grad_bias, void* workspace,
+                                 size_t workspace_bytes, void* stream);
 
 /* Static, human-readable name of a status code. */
 const char* qmoe_status_string(qmoe_status s);

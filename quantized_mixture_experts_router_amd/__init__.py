@@ -9,10 +9,17 @@ and the current stream.  The functions keep the C names:
     qmoe_noalloc_scratch_bytes, qmoe_status_string,
     qmoe_grouped_matmul_workspace_size, qmoe_grouped_matmul,
     qmoe_grouped_matmul_debug, qmoe_moe_attrs_default, qmoe_moe_validate,
-    qmoe_moe_workspace_size, qmoe_moe_forward, qmoe_moe_forward_debug
+    qmoe_moe_workspace_size, qmoe_moe_forward, qmoe_moe_forward_debug,
+    qmoe_route, qmoe_route_backward, qmoe_dispatch_workspace_size,
+    qmoe_dispatch, qmoe_dispatch_backward, qmoe_combine,
+    qmoe_combine_backward, qmoe_linear_attrs_default,
+    qmoe_linear_workspace_size, qmoe_linear,
+    qmoe_linear_backward_workspace_size, qmoe_linear_backward
 
 plus ``forward``, ``grouped_matmul`` and ``moe_forward`` (allocate output and
-workspace with torch, then call the entry point) for convenience.  The
+workspace with torch, then call the entry point) for convenience, and the
+same for the steps of a routed layer and their gradients: ``route``,
+``dispatch``, ``combine``, ``linear`` and their ``*_backward``.  The
 library is loaded on first use; a missing build raises immediately, there is
 no fallback.
 """
@@ -51,6 +58,12 @@ class QmoeMoeAttrs(ctypes.Structure):
     _fields_ = [("k", ctypes.c_int32), ("activation_type", ctypes.c_int32), ("swiglu_fusion", ctypes.c_int32),
                 ("activation_alpha", ctypes.c_float), ("activation_beta", ctypes.c_float),
                 ("normalize_routing_weights", ctypes.c_int32), ("use_sparse_mixer", ctypes.c_int32),
+                ("has_swiglu_limit", ctypes.c_int32), ("swiglu_limit", ctypes.c_float)]
+
+
+class QmoeLinearAttrs(ctypes.Structure):
+    _fields_ = [("activation_type", ctypes.c_int32), ("swiglu_fusion", ctypes.c_int32),
+                ("activation_alpha", ctypes.c_float), ("activation_beta", ctypes.c_float),
                 ("has_swiglu_limit", ctypes.c_int32), ("swiglu_limit", ctypes.c_float)]
 
 
@@ -122,6 +135,24 @@ def _lib():
         lib.qmoe_moe_forward_debug.argtypes = [T] * 8 + [MA, T, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p,
                                                          ctypes.POINTER(QmoeDebug)]
         lib.qmoe_moe_forward_debug.restype = ctypes.c_int
+        LA, I32, I64, P, Z = (ctypes.POINTER(QmoeLinearAttrs), ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p,
+                              ctypes.c_size_t)
+        ZP = ctypes.POINTER(ctypes.c_size_t)
+        for name, args in (("qmoe_route", [T, I32, I32, I32, T, T, P]),
+                           ("qmoe_route_backward", [T, T, T, I32, I32, T, P]),
+                           ("qmoe_dispatch_workspace_size", [T, T, I64, ZP]),
+                           ("qmoe_dispatch", [T, T, I64, T, T, T, T, P, Z, P]),
+                           ("qmoe_dispatch_backward", [T, T, T, P]),
+                           ("qmoe_combine", [T, T, T, T, P]),
+                           ("qmoe_combine_backward", [T] * 6 + [P]),
+                           ("qmoe_linear_workspace_size", [T] * 5 + [LA, T, T, ZP]),
+                           ("qmoe_linear", [T] * 5 + [LA, T, T, P, Z, P]),
+                           ("qmoe_linear_backward_workspace_size", [T] * 5 + [LA, T, T, T, ZP]),
+                           ("qmoe_linear_backward", [T] * 5 + [LA, T, T, T, P, Z, P])):
+            getattr(lib, name).argtypes = args
+            getattr(lib, name).restype = ctypes.c_int
+        lib.qmoe_linear_attrs_default.argtypes = [LA]
+        lib.qmoe_linear_attrs_default.restype = None
         lib.qmoe_status_string.argtypes = [ctypes.c_int]
         lib.qmoe_status_string.restype = ctypes.c_char_p
         _lib_handle = lib
@@ -439,3 +470,299 @@ def moe_forward(tensors: dict, attrs=None, stream=None, workspace=None, output=N
         workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=x.device)
     qmoe_moe_forward(tensors, attrs, output, workspace, stream, debug)
     return output
+
+
+# ------------------------------------------------------------------ steps of a routed layer
+class _on:
+    """The device of a call's tensors made current, and ``stream`` (or that
+    device's current stream) torch's stream, so that what torch allocates
+    belongs to the stream the work runs on.  All tensors lie on one device."""
+
+    def __init__(self, stream, tensors):
+        import torch
+        devices = {t.device for t in tensors if t is not None}
+        if len(devices) != 1 or next(iter(devices)).type != "cuda":
+            raise ValueError(f"qmoe tensors must be on one GPU, got {sorted(map(str, devices))}")
+        self.device = next(iter(devices))
+        if stream is not None and stream.device != self.device:
+            raise ValueError(f"stream of {stream.device}, tensors on {self.device}")
+        same = self.device.index == torch.cuda.current_device()
+        self.enter = ([] if same else [torch.cuda.device(self.device)]) + \
+            ([] if stream is None else [torch.cuda.stream(stream)])
+
+    def __enter__(self):
+        import torch
+        for c in self.enter:
+            c.__enter__()
+        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+
+    def __exit__(self, *exc):
+        for c in reversed(self.enter):
+            c.__exit__(*exc)
+
+
+def _ok(status, where):
+    if status != 0:
+        raise QmoeError(status, where)
+
+
+def _workspace(workspace, need, device):
+    """(pointer, bytes, tensor kept alive for the call) of a workspace of ``need`` bytes."""
+    import torch
+    if need == 0:
+        return None, 0, None
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def _route_args(attrs):
+    a = attrs if isinstance(attrs, QmoeAttrs) else make_attrs(attrs)
+    return a.k, a.routing, a.normalize_routing_weights
+
+
+def qmoe_route(router_probs, attrs, indices, weights, stream=None) -> None:
+    """Enqueue the routing weights: ``attrs`` holds k, routing and
+    normalize_routing_weights (those of ``forward``); indices int32 and
+    weights float32, both [T, k]."""
+    k, routing, norm = _route_args(attrs)
+    with _on(stream, (router_probs, indices, weights)) as st:
+        _ok(_lib().qmoe_route(_ref(router_probs, True), k, routing, norm, _ref(indices, True), _ref(weights, True), st),
+            "qmoe_route")
+
+
+def route(router_probs, attrs=None, stream=None, indices=None, weights=None):
+    """Allocate what is not given, then qmoe_route: (indices, weights)."""
+    import torch
+    k, routing, norm = _route_args(attrs)
+    with _on(stream, (router_probs, indices, weights)) as st:
+        shape = (router_probs.shape[0], max(int(k), 0))
+        if indices is None:
+            indices = torch.empty(shape, dtype=torch.int32, device=router_probs.device)
+        if weights is None:
+            weights = torch.empty(shape, dtype=torch.float32, device=router_probs.device)
+        _ok(_lib().qmoe_route(_ref(router_probs, True), k, routing, norm, _ref(indices, True), _ref(weights, True), st),
+            "qmoe_route")
+    return indices, weights
+
+
+def qmoe_route_backward(grad_weights, router_probs, indices, attrs, grad_router_probs, stream=None) -> None:
+    """Enqueue the gradient of qmoe_route at the logits (attrs: routing and
+    normalize_routing_weights; k is indices' second extent)."""
+    _, routing, norm = _route_args(attrs)
+    with _on(stream, (grad_weights, router_probs, indices, grad_router_probs)) as st:
+        _ok(_lib().qmoe_route_backward(_ref(grad_weights, True), _ref(router_probs, True), _ref(indices, True),
+                                       routing, norm, _ref(grad_router_probs, True), st), "qmoe_route_backward")
+
+
+def route_backward(grad_weights, router_probs, indices, attrs=None, stream=None, grad_router_probs=None):
+    """Allocate grad_router_probs [T, E] unless given, then qmoe_route_backward."""
+    import torch
+    _, routing, norm = _route_args(attrs)
+    with _on(stream, (grad_weights, router_probs, indices, grad_router_probs)) as st:
+        if grad_router_probs is None:
+            grad_router_probs = torch.empty_like(router_probs)
+        _ok(_lib().qmoe_route_backward(_ref(grad_weights, True), _ref(router_probs, True), _ref(indices, True),
+                                       routing, norm, _ref(grad_router_probs, True), st), "qmoe_route_backward")
+    return grad_router_probs
+
+
+def qmoe_dispatch_workspace_size(input, indices, experts) -> int:
+    """Workspace bytes of qmoe_dispatch.  Arrays may live anywhere."""
+    n = ctypes.c_size_t(0)
+    _ok(_lib().qmoe_dispatch_workspace_size(_ref(input, False), _ref(indices, False), int(experts), ctypes.byref(n)),
+        "qmoe_dispatch_workspace_size")
+    return int(n.value)
+
+
+def qmoe_dispatch(input, indices, experts, rows, offsets, perm, inverse, workspace=None, stream=None) -> None:
+    """Enqueue the sort of the slots by expert and the copy of their tokens'
+    rows; ``perm`` may be None, ``workspace`` too when its size is 0."""
+    with _on(stream, (input, indices, rows, offsets, perm, inverse, workspace)) as st:
+        p, n, _keep = _workspace(workspace, 0 if workspace is None else 1, input.device)
+        _ok(_lib().qmoe_dispatch(_ref(input, True), _ref(indices, True), int(experts), _ref(rows, True),
+                                 _ref(offsets, True), _ref(perm, True), _ref(inverse, True), p, n, st),
+            "qmoe_dispatch")
+
+
+def dispatch(input, indices, experts, stream=None, workspace=None):
+    """Allocate and qmoe_dispatch: (rows [T k, H], offsets [experts + 1], perm [T k], inverse [T, k])."""
+    import torch
+    with _on(stream, (input, indices, workspace)) as st:
+        need = qmoe_dispatch_workspace_size(input, indices, experts)
+        dev = input.device
+        T, k = indices.shape
+        rows = torch.empty((T * k, input.shape[1]), dtype=input.dtype, device=dev)
+        offsets = torch.empty(experts + 1, dtype=torch.int32, device=dev)
+        perm = torch.empty(T * k, dtype=torch.int32, device=dev)
+        inverse = torch.empty((T, k), dtype=torch.int32, device=dev)
+        p, n, _keep = _workspace(workspace, need, dev)
+        _ok(_lib().qmoe_dispatch(_ref(input, True), _ref(indices, True), int(experts), _ref(rows, True),
+                                 _ref(offsets, True), _ref(perm, True), _ref(inverse, True), p, n, st),
+            "qmoe_dispatch")
+    return rows, offsets, perm, inverse
+
+
+def qmoe_dispatch_backward(grad_rows, inverse, grad_input, stream=None) -> None:
+    """Enqueue the gradient of qmoe_dispatch at its input."""
+    with _on(stream, (grad_rows, inverse, grad_input)) as st:
+        _ok(_lib().qmoe_dispatch_backward(_ref(grad_rows, True), _ref(inverse, True), _ref(grad_input, True), st),
+            "qmoe_dispatch_backward")
+
+
+def dispatch_backward(grad_rows, inverse, stream=None, grad_input=None):
+    """Allocate grad_input [T, H] unless given, then qmoe_dispatch_backward."""
+    import torch
+    with _on(stream, (grad_rows, inverse, grad_input)) as st:
+        if grad_input is None:
+            grad_input = torch.empty((inverse.shape[0], grad_rows.shape[1]), dtype=grad_rows.dtype,
+                                     device=grad_rows.device)
+        _ok(_lib().qmoe_dispatch_backward(_ref(grad_rows, True), _ref(inverse, True), _ref(grad_input, True), st),
+            "qmoe_dispatch_backward")
+    return grad_input
+
+
+def qmoe_combine(rows, inverse, weights, output, stream=None) -> None:
+    """Enqueue the weighted sum of each token's rows (weights None: 1)."""
+    with _on(stream, (rows, inverse, weights, output)) as st:
+        _ok(_lib().qmoe_combine(_ref(rows, True), _ref(inverse, True), _ref(weights, True), _ref(output, True), st),
+            "qmoe_combine")
+
+
+def combine(rows, inverse, weights=None, stream=None, output=None):
+    """Allocate output [T, H] unless given, then qmoe_combine."""
+    import torch
+    with _on(stream, (rows, inverse, weights, output)) as st:
+        if output is None:
+            output = torch.empty((inverse.shape[0], rows.shape[1]), dtype=rows.dtype, device=rows.device)
+        _ok(_lib().qmoe_combine(_ref(rows, True), _ref(inverse, True), _ref(weights, True), _ref(output, True), st),
+            "qmoe_combine")
+    return output
+
+
+def qmoe_combine_backward(grad_output, rows, inverse, weights, grad_rows, grad_weights, stream=None) -> None:
+    """Enqueue the gradients of qmoe_combine (either may be None)."""
+    with _on(stream, (grad_output, rows, inverse, weights, grad_rows, grad_weights)) as st:
+        _ok(_lib().qmoe_combine_backward(_ref(grad_output, True), _ref(rows, True), _ref(inverse, True),
+                                         _ref(weights, True), _ref(grad_rows, True), _ref(grad_weights, True), st),
+            "qmoe_combine_backward")
+
+
+def combine_backward(grad_output, rows, inverse, weights, stream=None):
+    """Allocate and qmoe_combine_backward: (grad_rows, grad_weights)."""
+    import torch
+    with _on(stream, (grad_output, rows, inverse, weights)) as st:
+        grad_rows = torch.empty_like(rows)
+        grad_weights = torch.empty_like(weights)
+        _ok(_lib().qmoe_combine_backward(_ref(grad_output, True), _ref(rows, True), _ref(inverse, True),
+                                         _ref(weights, True), _ref(grad_rows, True), _ref(grad_weights, True), st),
+            "qmoe_combine_backward")
+    return grad_rows, grad_weights
+
+
+# ------------------------------------------------------------------ linear layers
+def qmoe_linear_attrs_default() -> QmoeLinearAttrs:
+    a = QmoeLinearAttrs()
+    _lib().qmoe_linear_attrs_default(ctypes.byref(a))
+    return a
+
+
+def make_linear_attrs(attrs: Optional[dict] = None) -> QmoeLinearAttrs:
+    """qmoe_linear_attrs from a dict of the float MoE's attribute names."""
+    a = qmoe_linear_attrs_default()
+    for key, val in (attrs or {}).items():
+        if key not in {f[0] for f in QmoeLinearAttrs._fields_}:
+            raise ValueError(f"no attribute {key!r} of a linear layer")
+        if key == "activation_type" and isinstance(val, str):
+            val = QMOE_ACT.get(val, 99)
+        elif key == "swiglu_limit":
+            a.has_swiglu_limit = 0 if val is None else 1
+            val = 0.0 if val is None else val
+        setattr(a, key, val)
+    return a
+
+
+def _linear_a(attrs):
+    return attrs if isinstance(attrs, QmoeLinearAttrs) else make_linear_attrs(attrs)
+
+
+def qmoe_linear_workspace_size(input, weights, bias=None, residual=None, offsets=None, attrs=None, output=None,
+                               preact=None) -> int:
+    """Workspace bytes of qmoe_linear.  Arrays may live anywhere."""
+    a, n = _linear_a(attrs), ctypes.c_size_t(0)
+    _ok(_lib().qmoe_linear_workspace_size(*[_ref(t, False) for t in (input, weights, bias, residual, offsets)],
+                                          ctypes.byref(a), _ref(output, False), _ref(preact, False), ctypes.byref(n)),
+        "qmoe_linear_workspace_size")
+    return int(n.value)
+
+
+def qmoe_linear(input, weights, bias, residual, offsets, attrs, output, preact=None, workspace=None,
+                stream=None) -> None:
+    """Enqueue a linear layer: input [M, K], weights [N, K] or [G, N, K] with
+    offsets [G + 1]; bias, residual and preact may be None, workspace too when
+    its size is 0."""
+    a = _linear_a(attrs)
+    with _on(stream, (input, weights, bias, residual, offsets, output, preact, workspace)) as st:
+        p, n, _keep = _workspace(workspace, 0 if workspace is None else 1, input.device)
+        _ok(_lib().qmoe_linear(*[_ref(t, True) for t in (input, weights, bias, residual, offsets)], ctypes.byref(a),
+                               _ref(output, True), _ref(preact, True), p, n, st), "qmoe_linear")
+
+
+def linear(input, weights, bias=None, residual=None, offsets=None, attrs=None, keep_preact=False, stream=None,
+           workspace=None, output=None):
+    """Allocate output (and preact with ``keep_preact``), then qmoe_linear:
+    output, or (output, preact)."""
+    import torch
+    a = _linear_a(attrs)
+    with _on(stream, (input, weights, bias, residual, offsets, workspace, output)) as st:
+        M, N = input.shape[0], weights.shape[-2]
+        No = N // 2 if a.activation_type == QMOE_ACT["swiglu"] else N
+        if output is None:
+            output = torch.empty((M, No), dtype=input.dtype, device=input.device)
+        preact = torch.empty((M, N), dtype=input.dtype, device=input.device) if keep_preact else None
+        need = qmoe_linear_workspace_size(input, weights, bias, residual, offsets, a, output, preact)
+        p, n, _keep = _workspace(workspace, need, input.device)
+        _ok(_lib().qmoe_linear(*[_ref(t, True) for t in (input, weights, bias, residual, offsets)], ctypes.byref(a),
+                               _ref(output, True), _ref(preact, True), p, n, st), "qmoe_linear")
+    return (output, preact) if keep_preact else output
+
+
+def qmoe_linear_backward_workspace_size(grad_output, input, weights, preact=None, offsets=None, attrs=None,
+                                        grad_input=None, grad_weights=None, grad_bias=None) -> int:
+    """Workspace bytes of qmoe_linear_backward for the gradients given.  Arrays may live anywhere."""
+    a, n = _linear_a(attrs), ctypes.c_size_t(0)
+    _ok(_lib().qmoe_linear_backward_workspace_size(
+        *[_ref(t, False) for t in (grad_output, input, weights, preact, offsets)], ctypes.byref(a),
+        *[_ref(t, False) for t in (grad_input, grad_weights, grad_bias)], ctypes.byref(n)),
+        "qmoe_linear_backward_workspace_size")
+    return int(n.value)
+
+
+def qmoe_linear_backward(grad_output, input, weights, preact, offsets, attrs, grad_input, grad_weights, grad_bias,
+                         workspace=None, stream=None) -> None:
+    """Enqueue the gradients of qmoe_linear (any may be None); preact None for
+    the identity, offsets None for a dense layer."""
+    a = _linear_a(attrs)
+    with _on(stream, (grad_output, input, weights, preact, offsets, grad_input, grad_weights, grad_bias,
+                      workspace)) as st:
+        p, n, _keep = _workspace(workspace, 0 if workspace is None else 1, input.device)
+        _ok(_lib().qmoe_linear_backward(
+            *[_ref(t, True) for t in (grad_output, input, weights, preact, offsets)], ctypes.byref(a),
+            *[_ref(t, True) for t in (grad_input, grad_weights, grad_bias)], p, n, st), "qmoe_linear_backward")
+
+
+def linear_backward(grad_output, input, weights, preact=None, offsets=None, attrs=None, bias=False, stream=None,
+                    workspace=None):
+    """Allocate and qmoe_linear_backward: (grad_input, grad_weights, grad_bias),
+    grad_bias None unless ``bias``."""
+    import torch
+    a = _linear_a(attrs)
+    with _on(stream, (grad_output, input, weights, preact, offsets, workspace)) as st:
+        gi, gw = torch.empty_like(input), torch.empty_like(weights)
+        gb = torch.empty(weights.shape[:-1], dtype=weights.dtype, device=weights.device) if bias else None
+        need = qmoe_linear_backward_workspace_size(grad_output, input, weights, preact, offsets, a, gi, gw, gb)
+        p, n, _keep = _workspace(workspace, need, input.device)
+        _ok(_lib().qmoe_linear_backward(
+            *[_ref(t, True) for t in (grad_output, input, weights, preact, offsets)], ctypes.byref(a),
+            *[_ref(t, True) for t in (gi, gw, gb)], p, n, st), "qmoe_linear_backward")
+    return gi, gw, gb

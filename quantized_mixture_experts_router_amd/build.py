@@ -21,6 +21,8 @@ SOURCES = [
     "qmoe_api.cpp",
     "qmoe_gmm.cpp",
     "qmoe_moe.cpp",
+    "qmoe_tokens.cpp",
+    "qmoe_linear.cpp",
     "kernels/route.hip",
     "kernels/operand.hip",
     "kernels/gemm.hip",
@@ -30,6 +32,11 @@ SOURCES = [
     "kernels/gmm.hip",
     "kernels/gmm_typed.hip",
     "kernels/moe.hip",
+    "kernels/tokens.hip",
+    "kernels/linear_ops.hip",
+    "kernels/linear_f16.hip",
+    "kernels/linear_bf16.hip",
+    "kernels/linear_f32.hip",
 ]
 
 ARCH = os.environ.get("QMOE_OFFLOAD_ARCH", "gfx950")

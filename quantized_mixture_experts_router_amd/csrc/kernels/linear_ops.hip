@@ -1,0 +1,240 @@
+// The linear layers' passes beside the matrix kernel (linear.h): the sum of
+// split reductions with the epilogue, the activation's gradient with column
+// sums, the bias gradient and row padding.  All are bound by HBM.
+#include "linear_common.hpp"
+
+namespace qmoe {
+
+namespace {
+
+// Group of output row m (rows behind the last group: G): binary search for
+// the first group whose end lies past m; offsets as find_block takes them.
+__device__ __forceinline__ int group_of_row(const int* __restrict__ offsets, int G, int M, int m) {
+  if (!offsets) return 0;
+  int a = 0, b = G;
+  while (a < b) {
+    const int c = (a + b) >> 1;
+    int lo, hi;
+    group_rows(offsets, G, M, c, lo, hi);
+    if (hi > m) b = c;
+    else a = c + 1;
+  }
+  return a;
+}
+
+// Four columns of one output row a thread: the ranges' sums added in range
+// order, then the epilogue (or the store).
+template <typename ET, int MODE, bool VEC>
+__global__ void __launch_bounds__(256) qmoe_linear_finish(const LinearGemm g) {
+  const int cols = MODE == LIN_FWD ? g.N : g.K;
+  const long ldp = (cols + 3) & ~3;
+  const long rows = MODE == LIN_DW ? (long)g.G * g.N : g.M;
+  const long i = (long)blockIdx.x * 256 + threadIdx.x;
+  const long row = i / (ldp >> 2);
+  const int c = (int)(i - row * (ldp >> 2)) * 4;
+  if (row >= rows) return;
+  int grp = 0;
+  if constexpr (MODE != LIN_DW) {
+    grp = group_of_row(g.offsets, g.G, g.M, (int)row);
+    if (grp >= g.G) {
+      if constexpr (MODE == LIN_FWD) linear_zero<ET>(g, (int)row, c);
+      else store_cols4<ET, false>(static_cast<ET*>(g.out) + row * g.K, c, g.K, f32x4{0.f, 0.f, 0.f, 0.f});
+      return;
+    }
+  }
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+  for (int s = 0; s < g.splits; ++s) v += *(const f32x4*)(g.partial + (s * rows + row) * ldp + c);
+  if constexpr (MODE == LIN_FWD) linear_epilogue<ET, VEC>(g, grp, (int)row, c, v);
+  else store_cols4<ET, VEC>(static_cast<ET*>(g.out) + row * g.K, c, g.K, v);
+}
+
+template <typename ET, int MODE>
+hipError_t go_finish(const LinearGemm& g, hipStream_t st) {
+  const long cols = MODE == LIN_FWD ? g.N : g.K;
+  const long rows = MODE == LIN_DW ? (long)g.G * g.N : g.M;
+  const long n = rows * ((cols + 3) / 4);
+  const dim3 grid((unsigned)((n + 255) / 256)), block(256);
+  if (linear_vec<ET>(g, MODE)) hipLaunchKernelGGL((qmoe_linear_finish<ET, MODE, true>), grid, block, 0, st, g);
+  else hipLaunchKernelGGL((qmoe_linear_finish<ET, MODE, false>), grid, block, 0, st, g);
+  return hipGetLastError();
+}
+
+template <typename ET>
+hipError_t finish_mode(int mode, const LinearGemm& g, hipStream_t st) {
+  if (mode == LIN_FWD) return go_finish<ET, LIN_FWD>(g, st);
+  if (mode == LIN_DX) return go_finish<ET, LIN_DX>(g, st);
+  return go_finish<ET, LIN_DW>(g, st);
+}
+
+// dz of kSumRows rows of one group by 4 * 64 columns a wavefront, four
+// columns a lane, and their column sums (float32, of the unrounded dz, in row
+// order: the four wavefronts take every fourth row each and add up in
+// wavefront order through LDS).
+template <typename ET, bool VEC>
+__global__ void __launch_bounds__(256) qmoe_linear_act_grad(const LinearActGrad g, int ncol) {
+  using V4 = typename LinVec4<ET>::type;
+  using V2 = typename LinVec2<ET>::type;
+  __shared__ f32x4 red[3][64];
+  const int rb = blockIdx.x / ncol;
+  int grp, lo, hi;
+  if (!find_block(g.offsets, g.G, g.M, kSumRows, rb, grp, lo, hi) || grp >= g.G) return;  // the whole workgroup
+  const int lane = lane_id(), wave = threadIdx.x >> 6;
+  const int n = (blockIdx.x % ncol) * 256 + 4 * lane;
+  const bool glu = g.act.type == kActSwiglu;
+  const long No = glu ? g.N >> 1 : g.N;
+  const int m1 = min(hi, lo + kSumRows);
+  const ET* dyp = static_cast<const ET*>(g.dy);
+  const ET* zp = static_cast<const ET*>(g.z);
+  f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+  for (int m = lo + wave; m < m1; m += 4) {
+    f32x4 dz = {0.f, 0.f, 0.f, 0.f};
+    if (VEC ? n < g.N : true) {
+      float z[4] = {0.f, 0.f, 0.f, 0.f}, dy[4] = {0.f, 0.f, 0.f, 0.f};
+      if constexpr (VEC) {
+        if (zp) {
+          const V4 t = *(const V4*)(zp + (long)m * g.N + n);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) z[i] = (float)t[i];
+        }
+        if (glu) {
+          const V2 t = *(const V2*)(dyp + (long)m * No + (n >> 1));
+          dy[0] = dy[1] = (float)t[0];
+          dy[2] = dy[3] = (float)t[1];
+        } else {
+          const V4 t = *(const V4*)(dyp + (long)m * No + n);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) dy[i] = (float)t[i];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (n + i < g.N) {
+            if (zp) z[i] = (float)zp[(long)m * g.N + n + i];
+            dy[i] = (float)dyp[(long)m * No + (glu ? (n + i) >> 1 : n + i)];
+          }
+      }
+      if (glu) {
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+          float a, b;
+          lin_swiglu_grad(dy[i], z[i], z[i + 1], g.act, a, b);
+          dz[i] = a;
+          dz[i + 1] = b;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dz[i] = lin_act_grad(dy[i], z[i], g.act);
+      }
+      if constexpr (!VEC) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (n + i >= g.N) dz[i] = 0.f;
+      }
+    }
+    if (g.dz) store_cols4<ET, VEC>(static_cast<ET*>(g.dz) + (long)m * g.lddz, n, (int)g.lddz, dz);
+    sum += dz;
+  }
+  if (!g.sums) return;
+  if (wave > 0) red[wave - 1][lane] = sum;
+  __syncthreads();
+  if (wave > 0) return;
+#pragma unroll
+  for (int w = 0; w < 3; ++w) sum += red[w][lane];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (n + i < g.N) g.sums[(long)rb * g.N + n + i] = sum[i];
+}
+
+template <typename ET>
+hipError_t go_act_grad(const LinearActGrad& g, hipStream_t st) {
+  auto al = [](const void* p, uintptr_t m) { return (reinterpret_cast<uintptr_t>(p) & m) == 0; };
+  const uintptr_t a4 = 4 * sizeof(ET) - 1;
+  const bool vec = g.N % 4 == 0 && al(g.z, a4) && al(g.dz, a4) &&
+                   al(g.dy, g.act.type == kActSwiglu ? 2 * sizeof(ET) - 1 : a4) && (!g.dz || g.lddz % 4 == 0) &&
+                   (!g.dz || g.lddz == g.N);
+  const long blocks = linear_sum_blocks(g.M, g.offsets ? g.G : -1);
+  const long cols = g.dz && g.lddz > g.N ? g.lddz : g.N;
+  const int ncol = (int)((cols + 255) / 256);
+  const dim3 grid((unsigned)(blocks * ncol)), block(256);
+  if (vec) hipLaunchKernelGGL((qmoe_linear_act_grad<ET, true>), grid, block, 0, st, g, ncol);
+  else hipLaunchKernelGGL((qmoe_linear_act_grad<ET, false>), grid, block, 0, st, g, ncol);
+  return hipGetLastError();
+}
+
+// One column a thread: the group's row blocks in order.
+template <typename ET>
+__global__ void __launch_bounds__(256) qmoe_linear_bias_grad(const float* __restrict__ sums,
+                                                             const int* __restrict__ offsets, int G, int M, int N,
+                                                             int ncol, int nblocks, ET* __restrict__ db) {
+  const int grp = blockIdx.x / ncol;
+  int first, count;
+  group_blocks(offsets, G, M, kSumRows, grp, first, count);
+  count = max(0, min(count, nblocks - first));  // (falling offsets)
+  const int n = (blockIdx.x % ncol) * 256 + threadIdx.x;
+  if (n >= N) return;
+  float s = 0.f;
+  const float* p = sums + (long)first * N + n;
+#pragma unroll 8
+  for (int i = 0; i < count; ++i) s += p[(long)i * N];
+  db[(long)grp * N + n] = (ET)s;
+}
+
+// cols elements of each row into rows of ld, zeros behind them: one thread an
+// element of the padded rows.
+template <typename U>
+__global__ void __launch_bounds__(256) qmoe_linear_pad(const U* __restrict__ src, long rows, int cols,
+                                                       U* __restrict__ dst, int ld) {
+  const int c = blockIdx.y * 256 + threadIdx.x;
+  if (c >= ld) return;
+  for (long r = blockIdx.x; r < rows; r += gridDim.x) dst[r * ld + c] = c < cols ? src[r * cols + c] : (U)0;
+}
+
+}  // namespace
+
+hipError_t launch_linear_finish(int type, int mode, const LinearGemm& g, hipStream_t st) {
+  if (type == LIN_F32) return finish_mode<float>(mode, g, st);
+  if (type == LIN_F16) return finish_mode<_Float16>(mode, g, st);
+  return finish_mode<__bf16>(mode, g, st);
+}
+
+hipError_t launch_linear_act_grad(int type, const LinearActGrad& g, hipStream_t st) {
+  if (type == LIN_F32) return go_act_grad<float>(g, st);
+  if (type == LIN_F16) return go_act_grad<_Float16>(g, st);
+  return go_act_grad<__bf16>(g, st);
+}
+
+hipError_t launch_linear_bias_grad(int type, const float* sums, const int* offsets, int G, int M, int N, void* db,
+                                   hipStream_t st) {
+  const int ncol = (N + 255) / 256, nblocks = (int)linear_sum_blocks(M, offsets ? G : -1);
+  const dim3 grid((unsigned)((long)G * ncol)), block(256);
+  if (type == LIN_F32)
+    hipLaunchKernelGGL(qmoe_linear_bias_grad<float>, grid, block, 0, st, sums, offsets, G, M, N, ncol, nblocks, (float*)db);
+  else if (type == LIN_F16)
+    hipLaunchKernelGGL(qmoe_linear_bias_grad<_Float16>, grid, block, 0, st, sums, offsets, G, M, N, ncol, nblocks, (_Float16*)db);
+  else
+    hipLaunchKernelGGL(qmoe_linear_bias_grad<__bf16>, grid, block, 0, st, sums, offsets, G, M, N, ncol, nblocks, (__bf16*)db);
+  return hipGetLastError();
+}
+
+hipError_t launch_linear_pad(int esize, const void* src, long rows, long cols, void* dst, long ld, hipStream_t st) {
+  const dim3 grid((unsigned)(rows < 65536 ? rows : 65536), (unsigned)((ld + 255) / 256)), block(256);
+  if (esize == 4)
+    hipLaunchKernelGGL(qmoe_linear_pad<uint32_t>, grid, block, 0, st, (const uint32_t*)src, rows, (int)cols,
+                       (uint32_t*)dst, (int)ld);
+  else
+    hipLaunchKernelGGL(qmoe_linear_pad<uint16_t>, grid, block, 0, st, (const uint16_t*)src, rows, (int)cols,
+                       (uint16_t*)dst, (int)ld);
+  return hipGetLastError();
+}
+
+hipError_t launch_linear_f16(int mode, int tile, const LinearGemm& g, hipStream_t st);
+hipError_t launch_linear_bf16(int mode, int tile, const LinearGemm& g, hipStream_t st);
+hipError_t launch_linear_f32(int mode, int tile, const LinearGemm& g, hipStream_t st);
+
+hipError_t launch_linear(int type, int mode, int tile, const LinearGemm& g, hipStream_t st) {
+  if (type == LIN_F32) return launch_linear_f32(mode, tile, g, st);
+  if (type == LIN_F16) return launch_linear_f16(mode, tile, g, st);
+  return launch_linear_bf16(mode, tile, g, st);
+}
+
+}  // namespace qmoe

@@ -1,0 +1,47 @@
+// Routing weights, tokens sorted by expert and back, each with its gradient:
+// launch functions (host side; enqueue only).
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace qmoe {
+
+enum RowType { ROW_F32 = 0, ROW_F16 = 1, ROW_BF16 = 2 };
+
+// k largest logits of each row (idx, -1 where masked experts are all that is
+// left) and their softmax weights, over the selection or (over_all) over
+// every expert.
+hipError_t launch_route_topk(const float* logits, int T, int E, int k, bool over_all, int* idx, float* w,
+                             hipStream_t st);
+hipError_t launch_route_grad(const float* gw, const float* logits, const void* idx, bool idx64, int T, int E, int k,
+                             bool over_all, float* gl, hipStream_t st);
+
+// Slots per block of the expert sort, and its block count, for S slots.
+constexpr int kSortRound = 512;
+inline int sort_chunk(long S) {
+  const long c = (S + 255) / 256;  // at most 256 blocks (each adds up the others' counts)
+  const long least = S <= 4096 ? 4096 : 1024;
+  const long v = c > least ? c : least;
+  return (int)((v + kSortRound - 1) / kSortRound * kSortRound);
+}
+// Stable sort of the S slots by expert: offsets [E + 1], perm [S] (may be
+// NULL), inverse [S] (place, or -1 - place of a slot whose index lies outside
+// [0, E): those follow the last expert, in slot order).  hist: nchunks x
+// (E + 1) ints when there is more than one block.
+hipError_t launch_sort_slots(const void* idx, bool idx64, int S, int E, int* hist, int* offsets, int* perm,
+                             int* inverse, hipStream_t st);
+
+// Rows of H elements.  dispatch: rows[place of (t, s)] = x[t], zeros at the
+// places of dropped slots.
+hipError_t launch_dispatch_rows(int type, const void* x, const int* inverse, int T, int k, long H, void* rows,
+                                hipStream_t st);
+// out[t] = sum_s w[t, s] rows[inverse[t, s]] (w NULL: 1), slots in order,
+// dropped ones and places outside [0, T k) left out.
+hipError_t launch_combine_rows(int type, const void* rows, const int* inverse, const float* w, int T, int k, long H,
+                               void* out, hipStream_t st);
+// grows[inverse[t, s]] = w[t, s] gout[t], gw[t, s] = <gout[t], rows[inverse[t, s]]>; zeros for dropped slots.
+// grows or gw may be NULL.
+hipError_t launch_combine_grad(int type, const void* gout, const void* rows, const int* inverse, const float* w,
+                               int T, int k, long H, void* grows, float* gw, hipStream_t st);
+
+}  // namespace qmoe

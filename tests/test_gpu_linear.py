@@ -1,0 +1,268 @@
+"""GPU parity of the linear layers and their gradients with the float64
+oracle, per element to the bounds of steps_util (stated before any run)."""
+import numpy as np
+import pytest
+
+import quantized_mixture_experts_router_amd as qm
+from oracle import steps_oracle as S
+
+import steps_util as U
+
+pytestmark = pytest.mark.gpu
+
+TYPES = ["float32", "float16", "bfloat16"]
+ACTS = [("identity", {}), ("relu", {}), ("gelu", {}), ("silu", {}), ("swiglu", {}),
+        ("swiglu", dict(alpha=1.7, beta=0.5, limit=0.8))]
+
+
+@pytest.fixture(scope="module")
+def torch():
+    import torch as _t
+    if not _t.cuda.is_available():
+        pytest.skip("no GPU")
+    return _t
+
+
+def attrs_of(kind, a):
+    d = {"activation_type": kind, "swiglu_fusion": int(kind == "swiglu")}
+    if "alpha" in a:
+        d.update(activation_alpha=a["alpha"], activation_beta=a["beta"], swiglu_limit=a["limit"])
+    return d
+
+
+def make(torch, dt, M, K, N, counts=None, kind="identity", bias=True, residual=False, seed=0):
+    r = np.random.default_rng(seed)
+    No = N // 2 if kind == "swiglu" else N
+    lead = () if counts is None else (len(counts),)
+    c = {}
+    c["x"], c["fx"] = U.typed(torch, r.standard_normal((M, K)), dt)
+    c["w"], c["fw"] = U.typed(torch, r.standard_normal((*lead, N, K)) / max(K, 1) ** 0.5, dt)
+    c["b"], c["fb"] = U.typed(torch, r.standard_normal((*lead, N)) * 0.1 if bias else None, dt)
+    c["r"], c["fr"] = U.typed(torch, r.standard_normal((M, No)) if residual else None, dt)
+    c["dy"], c["fdy"] = U.typed(torch, r.standard_normal((M, No)), dt)
+    c["z"], c["fz"] = U.typed(torch, None if kind == "identity" else r.standard_normal((M, N)), dt)
+    c["off"], c["foff"] = None, None
+    if counts is not None:
+        c["foff"] = np.concatenate([[0], np.cumsum(counts)]).astype(np.int64)
+        c["off"] = torch.tensor(c["foff"], dtype=torch.int32, device="cuda")
+    return c
+
+
+def ws_of(torch, n):
+    return torch.full((max(n, 1),), 0xFF, dtype=torch.uint8, device="cuda")
+
+
+def run_forward(torch, c, attrs, keep=True, stream=None):
+    M, N = c["x"].shape[0], c["w"].shape[-2]
+    No = c["dy"].shape[1]
+    y = torch.full((M, No), float("nan"), dtype=c["x"].dtype, device="cuda")
+    z = torch.full((M, N), float("nan"), dtype=c["x"].dtype, device="cuda") if keep else None
+    need = qm.qmoe_linear_workspace_size(c["x"], c["w"], c["b"], c["r"], c["off"], attrs, y, z)
+    qm.qmoe_linear(c["x"], c["w"], c["b"], c["r"], c["off"], attrs, y, z, ws_of(torch, need), stream)
+    return y, z
+
+
+def check_forward(torch, c, dt, kind, a, label, keep=True):
+    U.say(f"[linear {dt}] {label}")
+    y, z = run_forward(torch, c, attrs_of(kind, a), keep)
+    torch.cuda.synchronize()
+    ry, rz = S.linear(c["fx"], c["fw"], c["fb"], c["fr"], c["foff"], kind, **a)
+    A = S.preact(np.abs(c["fx"]), np.abs(c["fw"]), None if c["fb"] is None else np.abs(c["fb"]), c["foff"])
+    ez = U.sum_bound(c["fx"].shape[1], A)
+    if keep:
+        U.check(U.back(z), rz, np.where(A > 0, U.rounded(dt, rz, ez), 0.0) if c["foff"] is not None else
+                U.rounded(dt, rz, ez), "preact")
+    ey = U.act_bound(rz, ez, ry, kind, **a)
+    if c["fr"] is not None:  # one more float32 addition
+        ey = ey + 2.0 ** -23 * (np.abs(ry) + np.abs(c["fr"]) + ey)
+    n = S.live_rows(len(ry), c["fw"], c["foff"])
+    bound = U.rounded(dt, ry, ey)
+    bound[n:] = 0.0  # rows behind the last group are exactly zero
+    U.check(U.back(y), ry, bound, "output")
+
+
+def run_backward(torch, c, attrs, which=(True, True, True), stream=None):
+    gi = torch.full_like(c["x"], float("nan")) if which[0] else None
+    gw = torch.full_like(c["w"], float("nan")) if which[1] else None
+    gb = torch.full(c["w"].shape[:-1], float("nan"), dtype=c["x"].dtype, device="cuda") if which[2] else None
+    need = qm.qmoe_linear_backward_workspace_size(c["dy"], c["x"], c["w"], c["z"], c["off"], attrs, gi, gw, gb)
+    qm.qmoe_linear_backward(c["dy"], c["x"], c["w"], c["z"], c["off"], attrs, gi, gw, gb, ws_of(torch, need), stream)
+    return gi, gw, gb
+
+
+def check_backward(torch, c, dt, kind, a, label, which=(True, True, True)):
+    U.say(f"[linear grad {dt}] {label}")
+    got = run_backward(torch, c, attrs_of(kind, a), which)
+    torch.cuda.synchronize()
+    dx, dw, db, d = S.linear_grad(c["fdy"], c["fx"], c["fw"], c["fz"], c["foff"], kind, **a)
+    ed = U.grad_eval_bound(c["fdy"], c["fz"], kind, **a)
+    # d as the products' operand: evaluated in float32, then rounded to the type (not for the identity)
+    ed_op = ed if kind == "identity" else U.rounded(dt, d, ed)
+    absd = np.abs(d) + ed_op
+    # magnitudes and operand errors through the same sums
+    adx, adw, _, _ = S.linear_grad(absd, np.abs(c["fx"]), np.abs(c["fw"]), None, c["foff"])
+    edx, edw, edb, _ = S.linear_grad(ed_op, np.abs(c["fx"]), np.abs(c["fw"]), None, c["foff"])
+    _, _, adb, _ = S.linear_grad(np.abs(d) + ed, np.abs(c["fx"]), np.abs(c["fw"]), None, c["foff"])
+    _, _, edb, _ = S.linear_grad(ed, np.abs(c["fx"]), np.abs(c["fw"]), None, c["foff"])
+    M, N = d.shape
+    for g, ref, A, e, n, name in ((got[0], dx, adx, edx, N, "grad_input"), (got[1], dw, adw, edw, M, "grad_weights"),
+                                  (got[2], db, adb, edb, M, "grad_bias")):
+        if g is None:
+            continue
+        b = U.rounded(dt, ref, e + U.sum_bound(n, A))
+        b = np.where(A > 0, b, 0.0) if c["foff"] is not None else b
+        U.check(U.back(g), ref, b, name)
+
+
+# one row of tiles, ragged in all three, whole runs, over several tiles; with the ranges of a long reduction
+DENSE = [(1, 64, 128), (3, 33, 10), (70, 72, 130), (129, 200, 264), (300, 520, 136), (1, 4096, 512), (17, 2049, 66),
+         (33, 1, 2)]
+
+
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("M,K,N", DENSE)
+def test_dense(torch, dt, M, K, N):
+    for i, (kind, a) in enumerate(ACTS):
+        c = make(torch, dt, M, K, N, None, kind, bias=i % 2 == 0, residual=i % 3 == 0, seed=i)
+        check_forward(torch, c, dt, kind, a, f"{kind} {M}x{K}x{N}", keep=i % 2 == 1)
+        check_backward(torch, c, dt, kind, a, f"{kind} {M}x{K}x{N}")
+
+
+GROUPS = [([5, 0, 130, 1, 64], 0, 72, 136), ([0, 0, 3], 4, 40, 24), ([257, 300], 13, 128, 264), ([1] * 70, 2, 96, 130),
+          ([0, 0], 9, 64, 64), ([33], 0, 47, 38), ([200, 56, 500, 44], 40, 192, 520)]
+
+
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("counts,tail,K,N", GROUPS)
+def test_grouped(torch, dt, counts, tail, K, N):
+    M = sum(counts) + tail
+    for i, (kind, a) in enumerate(ACTS):
+        c = make(torch, dt, M, K, N, counts, kind, bias=i % 2 == 0, residual=i % 3 == 0, seed=10 + i)
+        if tail:  # what lies behind the last group is never read
+            for n in ("x", "r", "dy", "z"):
+                if c[n] is not None:
+                    c[n][M - tail:] = float("nan")
+                    c["f" + n][M - tail:] = 0.0
+        check_forward(torch, c, dt, kind, a, f"{kind} {counts[:6]} {K} {N}", keep=i % 2 == 1)
+        check_backward(torch, c, dt, kind, a, f"{kind} {counts[:6]} {K} {N}")
+
+
+@pytest.mark.parametrize("dt", ["float16", "bfloat16"])
+def test_large_tiles(torch, dt):
+    # 256 x 256 tiles in every product, ragged at their ends, dense and grouped
+    c = make(torch, dt, 2000, 1000, 3336, None, "silu", residual=True)
+    check_forward(torch, c, dt, "silu", {}, "2000x1000x3336")
+    check_backward(torch, c, dt, "silu", {}, "2000x1000x3336")
+    c = make(torch, dt, 1900, 1032, 2056, [1000, 300, 500], "swiglu")
+    check_forward(torch, c, dt, "swiglu", {}, "grouped 1900x1032x2056")
+    check_backward(torch, c, dt, "swiglu", {}, "grouped 1900x1032x2056")
+
+
+@pytest.mark.parametrize("which", [(True, False, False), (False, True, False), (False, False, True),
+                                   (True, False, True)])
+def test_gradients_one_by_one(torch, which):
+    c = make(torch, "bfloat16", 90, 50, 34, [40, 41], "gelu")
+    check_backward(torch, c, "bfloat16", "gelu", {}, str(which), which)
+
+
+@pytest.mark.parametrize("dt", TYPES)
+def test_empty(torch, dt):
+    # no rows: no output, zero weight and bias gradients
+    c = make(torch, dt, 0, 16, 24, None, "silu")
+    check_forward(torch, c, dt, "silu", {}, "no rows")
+    check_backward(torch, c, dt, "silu", {}, "no rows")
+    # no reduction: the bias alone; no columns: zero input gradient
+    c = make(torch, dt, 5, 0, 24, None, "silu")
+    check_forward(torch, c, dt, "silu", {}, "K = 0")
+    check_backward(torch, c, dt, "silu", {}, "K = 0")
+    c = make(torch, dt, 5, 16, 0, None, "identity")
+    check_forward(torch, c, dt, "identity", {}, "N = 0")
+    check_backward(torch, c, dt, "identity", {}, "N = 0")
+    # no groups: every row lies behind the last one
+    c = make(torch, dt, 5, 16, 24, [], "relu", residual=True)
+    check_forward(torch, c, dt, "relu", {}, "G = 0")
+    check_backward(torch, c, dt, "relu", {}, "G = 0")
+
+
+@pytest.mark.parametrize("dt", TYPES)
+def test_infinities_stay_in_their_row_and_column(torch, dt):
+    c = make(torch, dt, 40, 100, 72, None, "identity", bias=False)
+    c["x"][7, 3] = float("inf")
+    c["w"][5, 9] = float("nan")
+    y, _ = run_forward(torch, c, attrs_of("identity", {}))
+    g = U.back(y)
+    bad = ~np.isfinite(g)
+    assert bad[7].all() and bad[:, 5].all()
+    bad[7], bad[:, 5] = False, False
+    assert not bad.any()
+    # relu keeps a NaN; a large negative argument gives silu 0 and swiglu 0
+    c = make(torch, dt, 2, 8, 8, None, "relu", bias=False)
+    c["x"].zero_()
+    c["x"][0, 0] = float("nan")
+    assert np.isnan(U.back(run_forward(torch, c, attrs_of("relu", {}))[0])[0]).all()
+    for kind in ("silu", "gelu"):
+        c = make(torch, dt, 2, 8, 8, None, kind, bias=False)
+        c["x"].zero_()
+        c["x"][:, 0] = -30000.0
+        c["w"].zero_()
+        c["w"][:, 0] = 2.0 if dt == "float16" else 1e4
+        out = U.back(run_forward(torch, c, attrs_of(kind, {}), keep=False)[0])
+        assert np.all(out == 0.0), (kind, out)
+
+
+@pytest.mark.parametrize("dt", TYPES)
+def test_views_and_element_alignment(torch, dt):
+    # pointers aligned to their element only: rows of odd length are padded, others take element stores
+    c = make(torch, dt, 37, 45, 30, None, "gelu", residual=True)
+    for n in ("x", "w", "b", "r", "dy", "z"):
+        buf = torch.empty(c[n].numel() + 1, dtype=c[n].dtype, device="cuda")
+        v = buf[1:].view(c[n].shape)
+        v.copy_(c[n])
+        c[n] = v
+    check_forward(torch, c, dt, "gelu", {}, "element-aligned")
+    check_backward(torch, c, dt, "gelu", {}, "element-aligned")
+    # whole runs: the operands must be 16-byte aligned
+    c = make(torch, dt, 4, 32, 16, None, "identity")
+    buf = torch.empty(c["x"].numel() + 1, dtype=c["x"].dtype, device="cuda")
+    c["x"] = buf[1:].view(c["x"].shape)
+    with pytest.raises(qm.QmoeError) as e:
+        run_forward(torch, c, attrs_of("identity", {}))
+    assert e.value.name == "ALIGN"
+
+
+def test_convenience_calls_streams_and_repeats(torch):
+    c = make(torch, "bfloat16", 300, 512, 256, [100, 150, 30], "swiglu")
+    a = attrs_of("swiglu", {})
+    y0, z0 = qm.linear(c["x"], c["w"], c["b"], None, c["off"], a, keep_preact=True)
+    g0 = qm.linear_backward(c["dy"], c["x"], c["w"], c["z"], c["off"], a, bias=True)
+    torch.cuda.synchronize()
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    # two calls at once on two streams, with their own workspaces, then again: the same bits
+    for _ in range(2):
+        y1, z1 = qm.linear(c["x"], c["w"], c["b"], None, c["off"], a, keep_preact=True, stream=side)
+        g1 = qm.linear_backward(c["dy"], c["x"], c["w"], c["z"], c["off"], a, bias=True, stream=other)
+        torch.cuda.synchronize()
+        for p, q in zip((y0, z0, *g0), (y1, z1, *g1)):
+            assert torch.equal(p, q)
+
+
+@pytest.mark.parametrize("M", [1, 300])
+def test_graph(torch, M):
+    c = make(torch, "float16", M, 1024, 192, None, "silu", residual=True)
+    a = attrs_of("silu", {})
+    eager = [run_forward(torch, c, a), run_backward(torch, c, a)]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        f = run_forward(torch, c, a)
+        b = run_backward(torch, c, a)
+    for i in range(3):
+        for t in (*f, *b):
+            t.fill_(float("nan"))
+        c["x"].mul_(1.0 if i < 2 else 0.5)  # the replay reads what its inputs hold now
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        want = [*eager[0], *eager[1]] if i < 2 else [*run_forward(torch, c, a), *run_backward(torch, c, a)]
+        for p, q in zip(want, (*f, *b)):
+            assert torch.equal(p, q), i

@@ -1,0 +1,225 @@
+"""Refusals of the routed layer's steps, on the host: every contract check
+runs before anything is enqueued, so wrong calls return their status here
+without a GPU (pointers are never dereferenced by a refused call)."""
+import ctypes
+import os
+
+import numpy as np
+import pytest
+
+import quantized_mixture_experts_router_amd as qm
+
+NULL, SHAPE, ATTR, UNSUPPORTED, WORKSPACE, DTYPE, ALIGN = 1, 2, 3, 4, 5, 7, 8
+F32, I32, I64, F16, BF16, F64, U8 = qm.QMOE_F32, qm.QMOE_I32, qm.QMOE_I64, qm.QMOE_F16, qm.QMOE_BF16, qm.QMOE_F64, \
+    qm.QMOE_U8
+GOOD = 1 << 20  # an aligned pointer that nothing follows
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(qm.LIB_PATH):
+        pytest.skip("libqmoe.so not built (run __graft_entry__.build())")
+    return qm.library()
+
+
+def T(dtype, *dims, ptr=GOOD):
+    t = qm.QmoeTensor()
+    t.data, t.dtype, t.rank = ptr, dtype, len(dims)
+    for i, d in enumerate(dims[:3]):
+        t.dims[i] = d
+    return t
+
+
+def R(t):
+    return None if t is None else ctypes.byref(t)
+
+
+# ------------------------------------------------------------------ route
+def _route(lib, probs=T(F32, 5, 8), k=2, routing=0, norm=0, idx=T(I32, 5, 2), w=T(F32, 5, 2)):
+    return lib.qmoe_route(R(probs), k, routing, norm, R(idx), R(w), None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(probs=None), NULL), (dict(idx=None), NULL), (dict(w=None), NULL),
+    (dict(probs=T(F32, 5, 8, 1)), SHAPE), (dict(probs=T(F16, 5, 8)), DTYPE), (dict(probs=T(F32, -5, 8)), SHAPE),
+    (dict(k=0), ATTR), (dict(k=9), ATTR), (dict(routing=2), ATTR), (dict(norm=2), ATTR),
+    (dict(idx=T(I64, 5, 2)), DTYPE), (dict(w=T(F16, 5, 2)), DTYPE), (dict(idx=T(I32, 5, 3)), SHAPE),
+    (dict(w=T(F32, 4, 2)), SHAPE), (dict(probs=T(F32, 5, 1025)), UNSUPPORTED),
+    (dict(probs=T(F32, 1 << 30, 8)), UNSUPPORTED), (dict(probs=T(F32, 5, 8, ptr=None)), NULL),
+    (dict(probs=T(F32, 5, 8, ptr=GOOD + 2)), ALIGN), (dict(w=T(F32, 5, 2, ptr=GOOD + 1)), ALIGN)])
+def test_route_refusals(lib, kw, want):
+    assert _route(lib, **kw) == want
+
+
+def _route_back(lib, gw=T(F32, 5, 2), probs=T(F32, 5, 8), idx=T(I32, 5, 2), routing=0, norm=0, gl=T(F32, 5, 8)):
+    return lib.qmoe_route_backward(R(gw), R(probs), R(idx), routing, norm, R(gl), None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(gw=None), NULL), (dict(probs=None), NULL), (dict(idx=None), NULL), (dict(gl=None), NULL),
+    (dict(idx=T(I32, 5)), SHAPE), (dict(idx=T(I32, 5, 0)), ATTR), (dict(idx=T(I32, 5, 9)), ATTR),
+    (dict(idx=T(F32, 5, 2)), DTYPE), (dict(gw=T(F32, 5, 3)), SHAPE), (dict(gl=T(F32, 5, 7)), SHAPE),
+    (dict(gw=T(F16, 5, 2)), DTYPE), (dict(routing=-1), ATTR), (dict(idx=T(I64, 5, 2, ptr=GOOD + 4)), ALIGN)])
+def test_route_backward_refusals(lib, kw, want):
+    assert _route_back(lib, **kw) == want
+
+
+# ------------------------------------------------------------------ dispatch, combine
+def _dispatch(lib, x=T(BF16, 6, 10), idx=T(I32, 6, 2), experts=4, rows=T(BF16, 12, 10), off=T(I32, 5), perm=T(I32, 12),
+              inv=T(I32, 6, 2), ws=None, n=0):
+    return lib.qmoe_dispatch(R(x), R(idx), experts, R(rows), R(off), R(perm), R(inv), ws, n, None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(x=None), NULL), (dict(idx=None), NULL), (dict(rows=None), NULL), (dict(off=None), NULL),
+    (dict(inv=None), NULL), (dict(x=T(BF16, 6, 10, 1)), SHAPE), (dict(x=T(F64, 6, 10)), DTYPE),
+    (dict(x=T(U8, 6, 10)), DTYPE), (dict(x=T(BF16, 5, 10)), SHAPE), (dict(idx=T(F32, 6, 2)), DTYPE),
+    (dict(rows=T(F16, 12, 10)), DTYPE), (dict(rows=T(BF16, 11, 10)), SHAPE), (dict(off=T(I32, 4)), SHAPE),
+    (dict(off=T(I64, 5)), DTYPE), (dict(perm=T(I32, 11)), SHAPE), (dict(inv=T(I32, 12)), SHAPE),
+    (dict(experts=-1), ATTR), (dict(experts=1024), UNSUPPORTED), (dict(x=T(BF16, 6, 10, ptr=None)), NULL),
+    (dict(rows=T(BF16, 12, 10, ptr=GOOD + 1)), ALIGN), (dict(x=T(BF16, 6, -1)), SHAPE),
+    # 8192 slots need a workspace
+    (dict(x=T(BF16, 4096, 10), idx=T(I32, 4096, 2), rows=T(BF16, 8192, 10), perm=None, inv=T(I32, 4096, 2)), NULL),
+    (dict(x=T(BF16, 4096, 10), idx=T(I32, 4096, 2), rows=T(BF16, 8192, 10), perm=None, inv=T(I32, 4096, 2), ws=GOOD,
+          n=8), WORKSPACE),
+    (dict(x=T(BF16, 4096, 10), idx=T(I32, 4096, 2), rows=T(BF16, 8192, 10), perm=None, inv=T(I32, 4096, 2),
+          ws=GOOD + 64, n=1 << 20), ALIGN)])
+def test_dispatch_refusals(lib, kw, want):
+    assert _dispatch(lib, **kw) == want
+
+
+def test_dispatch_workspace(lib):
+    n = ctypes.c_size_t(7)
+    size = lambda t, k, e: lib.qmoe_dispatch_workspace_size(R(T(F32, t, 8)), R(T(I64, t, k)), e, ctypes.byref(n))  # noqa: E731
+    assert size(2048, 2, 64) == 0 and n.value == 0
+    assert size(2049, 2, 64) == 0 and n.value > 0
+    assert size(1 << 22, 8, 1023) == 0 and n.value <= 256 * 1024 * 4  # at most 256 blocks' counts
+    assert size(1 << 27, 8, 64) == UNSUPPORTED
+    assert lib.qmoe_dispatch_workspace_size(R(T(F32, 4, 8)), R(T(I64, 4, 1)), 4, None) == NULL
+
+
+def _combine(lib, rows=T(F16, 12, 10), inv=T(I32, 6, 2), w=T(F32, 6, 2), out=T(F16, 6, 10)):
+    return lib.qmoe_combine(R(rows), R(inv), R(w), R(out), None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(rows=None), NULL), (dict(inv=None), NULL), (dict(out=None), NULL), (dict(rows=T(F16, 12)), SHAPE),
+    (dict(inv=T(I64, 6, 2)), DTYPE), (dict(w=T(F16, 6, 2)), DTYPE), (dict(w=T(F32, 6, 3)), SHAPE),
+    (dict(out=T(F32, 6, 10)), DTYPE), (dict(out=T(F16, 6, 11)), SHAPE), (dict(rows=T(F16, 13, 10)), SHAPE),
+    (dict(rows=T(F64, 12, 10), out=T(F64, 6, 10)), DTYPE), (dict(out=T(F16, 6, 10, ptr=None)), NULL),
+    (dict(rows=T(F16, 12, 1 << 25), out=T(F16, 6, 1 << 25)), UNSUPPORTED)])
+def test_combine_refusals(lib, kw, want):
+    assert _combine(lib, **kw) == want
+
+
+def test_dispatch_backward_refusals(lib):
+    f = lambda g, i, o: lib.qmoe_dispatch_backward(R(g), R(i), R(o), None)  # noqa: E731
+    assert f(None, T(I32, 6, 2), T(F16, 6, 10)) == NULL
+    assert f(T(F16, 12, 10), T(I32, 6, 2), T(F16, 6, 9)) == SHAPE
+    assert f(T(F16, 12, 10), T(I32, 6, 2), T(BF16, 6, 10)) == DTYPE
+
+
+def _combine_back(lib, g=T(F32, 6, 10), rows=T(F32, 12, 10), inv=T(I32, 6, 2), w=T(F32, 6, 2), gr=T(F32, 12, 10),
+                  gw=T(F32, 6, 2)):
+    return lib.qmoe_combine_backward(R(g), R(rows), R(inv), R(w), R(gr), R(gw), None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(g=None), NULL), (dict(rows=None), NULL), (dict(inv=None), NULL), (dict(w=None), NULL),
+    (dict(gr=T(F32, 11, 10)), SHAPE), (dict(gr=T(F16, 12, 10)), DTYPE), (dict(gw=T(F32, 6, 1)), SHAPE),
+    (dict(gw=T(F16, 6, 2)), DTYPE), (dict(g=T(F32, 5, 10)), SHAPE), (dict(gw=T(F32, 6, 2, ptr=GOOD + 2)), ALIGN)])
+def test_combine_backward_refusals(lib, kw, want):
+    assert _combine_back(lib, **kw) == want
+
+
+# ------------------------------------------------------------------ linear
+def _a(**kw):
+    a = qm.qmoe_linear_attrs_default()
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+def test_linear_defaults(lib):
+    a = qm.qmoe_linear_attrs_default()
+    assert (a.activation_type, a.swiglu_fusion, a.activation_alpha, a.activation_beta, a.has_swiglu_limit) == \
+        (qm.QMOE_ACT["identity"], 0, 1.0, 0.0, 0)
+    with pytest.raises(ValueError):
+        qm.make_linear_attrs({"k": 2})
+
+
+SWIGLU = dict(activation_type=qm.QMOE_ACT["swiglu"], swiglu_fusion=1)
+
+
+def _linear(lib, x=T(BF16, 6, 16), w=T(BF16, 8, 16), b=T(BF16, 8), r=T(BF16, 6, 8), off=None, a={}, y=T(BF16, 6, 8),
+            z=None, ws=None, n=0):
+    return lib.qmoe_linear(R(x), R(w), R(b), R(r), R(off), R(_a(**a)) if a is not None else None, R(y), R(z), ws, n,
+                           None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(x=None), NULL), (dict(w=None), NULL), (dict(a=None), NULL), (dict(y=None), NULL),
+    (dict(x=T(BF16, 6, 16, 1)), SHAPE), (dict(w=T(BF16, 8)), SHAPE), (dict(w=T(BF16, 8, 15)), SHAPE),
+    (dict(x=T(F64, 6, 16), w=T(F64, 8, 16)), DTYPE), (dict(w=T(F16, 8, 16)), DTYPE), (dict(b=T(F32, 8)), DTYPE),
+    (dict(r=T(F32, 6, 8)), DTYPE), (dict(y=T(F16, 6, 8)), DTYPE), (dict(z=T(F32, 6, 8)), DTYPE),
+    (dict(b=T(BF16, 7)), SHAPE), (dict(b=T(BF16, 1, 8)), SHAPE), (dict(r=T(BF16, 6, 7)), SHAPE),
+    (dict(y=T(BF16, 5, 8)), SHAPE), (dict(z=T(BF16, 6, 4)), SHAPE), (dict(x=T(BF16, -1, 16)), SHAPE),
+    (dict(off=T(I32, 2)), SHAPE),                                  # offsets with one dense weight
+    (dict(w=T(BF16, 3, 8, 16), b=None), NULL),                     # one weight per group without offsets
+    (dict(w=T(BF16, 3, 8, 16), b=None, off=T(I32, 3)), SHAPE),
+    (dict(w=T(BF16, 3, 8, 16), b=None, off=T(I64, 4)), DTYPE),
+    (dict(w=T(BF16, 3, 8, 16), b=T(BF16, 2, 8), off=T(I32, 4)), SHAPE),
+    (dict(w=T(BF16, 1024, 8, 16), b=None, off=T(I32, 1025)), UNSUPPORTED),
+    (dict(a=dict(activation_type=5)), ATTR), (dict(a=dict(swiglu_fusion=3)), ATTR),
+    (dict(a=dict(activation_type=1, swiglu_fusion=0)), UNSUPPORTED),
+    (dict(a=dict(activation_type=1, swiglu_fusion=2)), UNSUPPORTED),
+    (dict(a=dict(SWIGLU, has_swiglu_limit=1, swiglu_limit=0.0)), ATTR),
+    (dict(a=dict(SWIGLU, has_swiglu_limit=1, swiglu_limit=float("nan"))), ATTR),
+    (dict(a=SWIGLU), SHAPE),                                       # output [6, 8], not [6, 4]
+    (dict(w=T(BF16, 7, 16), b=None, r=None, y=T(BF16, 6, 3), a=SWIGLU), SHAPE),  # odd gate / linear columns
+    (dict(x=T(BF16, 6, 1 << 21), w=T(BF16, 8, 1 << 21)), UNSUPPORTED),
+    (dict(x=T(BF16, (1 << 30) + 1, 16), y=T(BF16, (1 << 30) + 1, 8), r=None), UNSUPPORTED),
+    (dict(x=T(BF16, 6, 16, ptr=None)), NULL), (dict(y=T(BF16, 6, 8, ptr=None)), NULL),
+    (dict(x=T(BF16, 6, 16, ptr=GOOD + 2)), ALIGN), (dict(w=T(BF16, 8, 16, ptr=GOOD + 8)), ALIGN),
+    (dict(b=T(BF16, 8, ptr=GOOD + 1)), ALIGN),
+    (dict(x=T(BF16, 6, 15), w=T(BF16, 8, 15)), NULL),              # padded rows need a workspace
+    (dict(x=T(BF16, 6, 15), w=T(BF16, 8, 15), ws=GOOD, n=16), WORKSPACE),
+    (dict(x=T(BF16, 6, 15), w=T(BF16, 8, 15), ws=GOOD + 16, n=1 << 20), ALIGN)])
+def test_linear_refusals(lib, kw, want):
+    assert _linear(lib, **kw) == want
+
+
+def _back(lib, g=T(F32, 6, 8), x=T(F32, 6, 16), w=T(F32, 8, 16), z=None, off=None, a={}, gi=T(F32, 6, 16),
+          gw=T(F32, 8, 16), gb=T(F32, 8), ws=GOOD, n=1 << 20):
+    return lib.qmoe_linear_backward(R(g), R(x), R(w), R(z), R(off), R(_a(**a)) if a is not None else None, R(gi), R(gw),
+                                    R(gb), ws, n, None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(g=None), NULL), (dict(x=None), NULL), (dict(w=None), NULL), (dict(a=None), NULL),
+    (dict(a=dict(activation_type=qm.QMOE_ACT["silu"])), NULL),     # the pre-activation is needed
+    (dict(a=dict(activation_type=qm.QMOE_ACT["silu"]), z=T(F32, 6, 7)), SHAPE),
+    (dict(g=T(F32, 6, 7)), SHAPE), (dict(gi=T(F32, 6, 15)), SHAPE), (dict(gi=T(F16, 6, 16)), DTYPE),
+    (dict(gw=T(F32, 8, 15)), SHAPE), (dict(gw=T(F32, 1, 8, 16)), SHAPE), (dict(gb=T(F32, 9)), SHAPE),
+    (dict(gb=T(F16, 8)), DTYPE), (dict(g=T(F16, 6, 8)), DTYPE), (dict(g=T(F32, 6, 8, ptr=GOOD + 4)), ALIGN),
+    (dict(x=T(F32, 6, 16, ptr=GOOD + 4)), ALIGN), (dict(ws=None), NULL), (dict(n=4), WORKSPACE),
+    (dict(ws=GOOD + 4), ALIGN)])
+def test_linear_backward_refusals(lib, kw, want):
+    assert _back(lib, **kw) == want
+
+
+def test_linear_workspaces(lib):
+    x, w = np.zeros((4, 16), np.float16), np.zeros((8, 16), np.float16)
+    assert qm.qmoe_linear_workspace_size(x, w) == 0
+    assert qm.qmoe_linear_workspace_size(x[:, :15], w[:, :15]) == 256 + 256  # both operands in padded rows
+    with pytest.raises(qm.QmoeError) as e:
+        qm.qmoe_linear_workspace_size(x, w[:, :8])
+    assert e.value.name == "SHAPE"
+
+
+def test_calls_want_one_gpu(lib):
+    torch = pytest.importorskip("torch")
+    with pytest.raises(ValueError):
+        qm.linear(torch.zeros(2, 8), torch.zeros(4, 8))
+    with pytest.raises(ValueError):
+        qm.route(torch.zeros(2, 8), {"k": 1})
