@@ -8,18 +8,21 @@
 // (buffer loads to LDS: the buffer's size is the operand's own, so a row past
 // the group's end or a column past the row's reads as zero without a branch),
 // and a stage holds 128 bytes of r per row of a run-of-r operand (64 16-bit or
-// 32 32-bit values) or as many r rows of the other kind.
+// 32 32-bit values) or as many r rows of the other kind.  Pieces of 16 bytes
+// are permuted inside their row (the source address is; the LDS side of the
+// load is linear) so that the lanes that read together meet different banks:
+//  - run-of-r tiles, 128-byte rows, sixteen lanes read one piece of sixteen
+//    rows: piece c of row i in slot c ^ (i / 2 & 7);
+//  - the other kind, 16-bit: the transposing LDS read gives a lane four r of
+//    its column; its half-wavefronts read 32 bytes of rows r .. r + 3 and
+//    r + 8 .. r + 11: slot c ^ (4 (r & 3) + 2 (r / 8 & 1));
+//  - 32-bit values of the other kind are read one by one, 64 bytes of rows
+//    r, r + 4, r + 8, r + 12: slot c ^ 4 (r / 4 & 3).
 //
-//  - Run-of-r tiles: row i is 8 pieces of 16 bytes, piece c in slot c ^ (i & 7)
-//    (the source address is permuted, the LDS side of the load is linear), so
-//    that eight lanes reading one piece of eight rows meet every bank once.
-//  - The other kind, 16-bit: row r holds all BT columns; the transposing LDS
-//    read gives a lane four r of its column; pieces are rotated by 64 bytes a
-//    row so that the four rows of one read fall into different banks.  32-bit
-//    values are read one by one.
-//
-// The matrix instruction's row operand is P and its column operand Q, so a
-// lane ends with runs of four consecutive output columns of one output row.
+// The matrix instructions are the 16-row ones: at the card's power limit they
+// sustain 2.1 GHz where the 32-row ones do 1.8 (2170 against 1900 TFLOP/s in
+// registers).  Their row operand is P and their column operand Q, so a lane
+// ends with four consecutive output columns of one output row.
 #pragma once
 #include <type_traits>
 
@@ -28,22 +31,32 @@
 namespace qmoe {
 
 template <typename ET>
-struct LinMma {  // 16-bit: 32 x 32 x 16, eight r a lane
+struct LinMma {  // 16-bit: 16 x 16 x 32, eight r a lane
   using Frag = typename std::conditional<std::is_same<ET, _Float16>::value, h16x8, b16x8>::type;
-  static __device__ __forceinline__ f32x16 mma(Frag p, Frag q, f32x16 c) {
-    if constexpr (std::is_same<ET, _Float16>::value) return __builtin_amdgcn_mfma_f32_32x32x16_f16(p, q, c, 0, 0, 0);
-    else return __builtin_amdgcn_mfma_f32_32x32x16_bf16(p, q, c, 0, 0, 0);
+  static __device__ __forceinline__ f32x4 mma(Frag p, Frag q, f32x4 c) {
+    if constexpr (std::is_same<ET, _Float16>::value) return __builtin_amdgcn_mfma_f32_16x16x32_f16(p, q, c, 0, 0, 0);
+    else return __builtin_amdgcn_mfma_f32_16x16x32_bf16(p, q, c, 0, 0, 0);
   }
 };
 template <>
-struct LinMma<float> {  // 32 x 32 x 2, four steps over the four r a lane holds
+struct LinMma<float> {  // 16 x 16 x 4, four steps over the four r a lane holds
   using Frag = f32x4;
-  static __device__ __forceinline__ f32x16 mma(Frag p, Frag q, f32x16 c) {
+  static __device__ __forceinline__ f32x4 mma(Frag p, Frag q, f32x4 c) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_32x32x2f32(p[j], q[j], c, 0, 0, 0);
+    for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(p[j], q[j], c, 0, 0, 0);
     return c;
   }
 };
+
+// Wait until at most N vector-memory operations of this wavefront are in
+// flight and its LDS accesses are done.
+template <int N>
+__device__ __forceinline__ void lin_wait() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (0x7 << 4));
+  asm volatile("" ::: "memory");
+}
 
 #define QMOE_LDS(p) ((__attribute__((address_space(3))) void*)(p))
 
@@ -52,79 +65,91 @@ struct LinMma<float> {  // 32 x 32 x 2, four steps over the four r a lane holds
 template <typename ET, int BT, bool RUN, int NW>
 struct LinOperand {
   static constexpr int ES = sizeof(ET), EPC = 16 / ES, BK = 128 / ES;
-  static constexpr int kBytes = BT * 128;              // one stage
-  static constexpr int kLoads = kBytes / 1024 / NW;    // load instructions of a wavefront and stage
-  static constexpr int CPR = BT * ES / 16;             // pieces per r row
-  static constexpr int RPI = RUN ? 8 : 64 / CPR;       // rows one instruction covers
-  static_assert(kBytes % (1024 * NW) == 0, "every wavefront issues the same count");
+  static constexpr int kBytes = BT * 128;            // one stage
+  static constexpr int kLoads = kBytes / 1024 / NW;  // load instructions of a wavefront and stage
+  static constexpr int CPR = BT * ES / 16;           // pieces per r row
+  static constexpr int RPI = RUN ? 8 : 64 / CPR;     // rows one instruction covers
+  // the permutation depends on r mod 16: lane offsets that repeat over a
+  // wavefront's instructions
+  static constexpr int kOffs = RUN || RPI * NW >= 16 ? 1 : 16 / (RPI * NW);
+  static_assert(kBytes % (1024 * NW) == 0 && NW % 2 == 0, "every wavefront issues the same count");
+  static_assert(kLoads % kOffs == 0 || kLoads < kOffs, "the offsets repeat");
+  static constexpr int kOut = (int)0x80000000;  // an offset past every buffer
 
-  const char* base;  // tile's first row or column at r = 0
+  const char* base;  // stage's first row or column, at the stage's first r
   long left;         // bytes from base to the end of the operand's rows
-  long step;         // bytes from stage to stage
   int ldb;           // row stride in bytes
-  int voff;          // this lane's offset in an instruction's rows
-  int piece;         // RUN: this lane's piece of its row
+  int voff[kOffs];   // this lane's offset in an instruction's rows
+  int piece;         // RUN: first r of this lane's piece in its stage
 
   static __device__ __forceinline__ int swz(int r) {
-    if constexpr (ES == 4 || CPR < 8) return 0;  // (64-byte rows: four differ by themselves)
-    if constexpr (CPR >= 16) return (r & 3) << 2;
-    return ((r >> 1) & 1) << 2;  // 128-byte rows: neighbours already differ
+    if constexpr (ES == 4) return CPR >= 16 ? ((r >> 2) & 3) << 2 : ((r >> 2) & 1) << 2;
+    const int h = ((r >> 3) & 1) << 1;
+    if constexpr (CPR >= 16) return ((r & 3) << 2) | h;
+    if constexpr (CPR == 8) return (((r >> 1) & 1) << 2) | h;  // 128-byte rows: neighbours already differ
+    return h;                                                  // 64-byte rows: four differ by themselves
   }
 
   // src: element (0, 0) of the tile; ld: row stride in elements; rows: RUN,
-  // valid rows, else valid r; cols: RUN, unused, else valid columns from the
-  // tile's first
-  __device__ __forceinline__ void init(const ET* src, long ld, long rows, long row_len, int cols, int lane) {
-    base = reinterpret_cast<const char*>(src);
+  // valid rows, else valid r; row_len: elements from src to its row's end;
+  // cols: else, valid columns from the tile's first; kb: first stage
+  __device__ __forceinline__ void init(const ET* src, long ld, long rows, long row_len, int cols, long kb, int wave,
+                                       int lane) {
     ldb = (int)(ld * ES);
-    left = rows > 0 ? ((rows - 1) * ld + row_len) * ES : 0;
+    const long at = kb * (RUN ? 128 : (long)BK * ldb);
+    base = reinterpret_cast<const char*>(src) + at;
+    left = rows > 0 ? ((rows - 1) * ld + row_len) * ES - at : 0;
     if constexpr (RUN) {
-      step = 128;
-      piece = (lane & 7) ^ (lane >> 3);
-      voff = (lane >> 3) * ldb + piece * 16;
+      // row / 2 of row 8 (i NW + wave) + lane / 8, NW even
+      const int c = (lane & 7) ^ (4 * (wave & 1) + (lane >> 4));
+      piece = c * EPC;
+      voff[0] = (lane >> 3) * ldb + c * 16;
     } else {
-      step = (long)BK * ldb;
-      const int r = lane / CPR;  // + a multiple of RPI: the same r & 3 (see issue)
       piece = 0;
-      voff = r * ldb;
-      (void)cols;
+#pragma unroll
+      for (int i = 0; i < kOffs; ++i) {
+        const int c = (lane % CPR) ^ swz((i * NW + wave) * RPI + lane / CPR);
+        voff[i] = c * EPC < cols ? lane / CPR * ldb + c * 16 : kOut;
+      }
     }
   }
 
-  // Stage kt (r from kt * BK, of R) into LDS at dst.
-  __device__ __forceinline__ void issue(char* dst, long kt, long R, int cols, int wave, int lane) const {
-    long rem = left - kt * step;
-    rem = rem < 0 ? 0 : rem > 0x7fffffff ? 0x7fffffff : rem;
+  // The next stage into LDS at dst; r0 = its first r (of R); not on: past the
+  // range of r, nothing is read and the stage fills with zeros.
+  __device__ __forceinline__ void issue(char* dst, int r0, int R, bool on, int wave) {
+    const long rem = on ? left : 0;
     const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<char*>(base + kt * step), 0, (int)rem, 0x00027000);
+        const_cast<char*>(base), 0, (int)(rem < 0 ? 0 : rem > 0x7fffffff ? 0x7fffffff : rem), 0x00027000);
+    // the last stage: pieces from R on are out of range, not the next row
+    const int v0 = RUN && r0 + piece >= R ? kOut : voff[0];
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const int idx = i * NW + wave;
-      int vo = voff;
-      if constexpr (RUN) {
-        // the last stage: pieces from R on are out of range, not the next row
-        if (kt * BK + piece * EPC >= R) vo = (int)0x80000000;
-      } else {
-        const int r = idx * RPI + lane / CPR;
-        const int c = (lane % CPR) ^ swz(r);
-        vo = c * EPC < cols ? voff + c * 16 : (int)0x80000000;
-      }
+      int vo = v0;
+      if constexpr (kOffs > 1) vo = voff[i % kOffs];
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, QMOE_LDS(dst + idx * 1024), 16, vo, idx * RPI * ldb, 0, 0);
     }
+    const long step = RUN ? 128 : (long)BK * ldb;
+    base += step;
+    left -= step;
   }
 
-  // This lane's operand of k step ks (16 16-bit or 8 32-bit r) for the 32
-  // rows or columns from t0 on.
+  // This lane's operand of k step ks (32 16-bit or 16 32-bit r) for the 16
+  // rows or columns from t0 on: r = 8 (lane / 16) .. + 7 of the step (32-bit:
+  // 4 (lane / 16) .. + 3).
   static __device__ __forceinline__ typename LinMma<ET>::Frag frag(const char* src, int t0, int ks, int lane) {
     using Frag = typename LinMma<ET>::Frag;
     if constexpr (RUN) {
-      const int c = 2 * ks + (lane >> 5);
-      return *(const Frag*)(src + (t0 + (lane & 31)) * 128 + ((c ^ (lane & 7)) << 4));
+      const int c = 4 * ks + (lane >> 4);
+      return *(const Frag*)(src + (t0 + (lane & 15)) * 128 + ((c ^ ((lane >> 1) & 7)) << 4));
     } else if constexpr (ES == 4) {
       Frag f;
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        f[j] = *(const float*)(src + (8 * ks + 4 * (lane >> 5) + j) * (BT * 4) + (t0 + (lane & 31)) * 4);
+      for (int j = 0; j < 4; ++j) {
+        const int r = 16 * ks + 4 * (lane >> 4) + j;
+        const int c = ((t0 >> 2) + ((lane & 15) >> 2)) ^ swz(r);
+        f[j] = *(const float*)(src + r * (BT * 4) + (c << 4) + (lane & 3) * 4);
+      }
       return f;
     } else {
       union {
@@ -133,10 +158,10 @@ struct LinOperand {
       } u;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int r = 16 * ks + 8 * (lane >> 5) + 4 * h + ((lane & 15) >> 2);
-        const int c = (t0 >> 3) + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+        const int r = 32 * ks + 8 * (lane >> 4) + 4 * h + ((lane & 15) >> 2);
+        const int c = ((t0 >> 3) + ((lane & 3) >> 1)) ^ swz(r);
         u.h[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (__attribute__((address_space(3))) s16x4*)(src + r * (BT * 2) + ((c ^ swz(r)) << 4) + (lane & 1) * 8));
+            (__attribute__((address_space(3))) s16x4*)(src + r * (BT * 2) + (c << 4) + (lane & 1) * 8));
       }
       return u.f;
     }
@@ -156,10 +181,10 @@ __device__ __forceinline__ void tile_of(int b, int nq, int np, int& q, int& p) {
 
 template <typename ET, int MODE, int BQ, int BP, int WQ, int WP, int NST, bool VEC>
 __global__ void __launch_bounds__(64 * WQ * WP) qmoe_linear(const LinearGemm g, int nq, int np) {
-  constexpr int NW = WQ * WP, TQ = BQ / WQ / 32, TP = BP / WP / 32;
+  constexpr int NW = WQ * WP, TQ = BQ / WQ / 16, TP = BP / WP / 16;
   using OP = LinOperand<ET, BP, MODE == LIN_FWD, NW>;
   using OQ = LinOperand<ET, BQ, MODE != LIN_DW, NW>;
-  constexpr int BK = OP::BK, KS = BK / (sizeof(ET) == 4 ? 8 : 16);
+  constexpr int BK = OP::BK, KS = 2;
   __shared__ __attribute__((aligned(1024))) char lds[NST][OP::kBytes + OQ::kBytes];
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
@@ -172,7 +197,7 @@ __global__ void __launch_bounds__(64 * WQ * WP) qmoe_linear(const LinearGemm g, 
   if (p0 >= pcols) return;
   OP op;
   OQ oq;
-  long R;
+  int R;
   if constexpr (MODE == LIN_DW) {
     const int nqg = (g.N + BQ - 1) / BQ;  // q blocks of a group
     grp = qb / nqg;
@@ -181,8 +206,6 @@ __global__ void __launch_bounds__(64 * WQ * WP) qmoe_linear(const LinearGemm g, 
     qrows = g.N - q0;
     group_rows(g.offsets, g.G, g.M, grp, lo, hi);
     R = hi - lo;
-    op.init(static_cast<const ET*>(g.x) + (long)lo * g.ldx + p0, g.ldx, R, g.ldx - p0, g.K - p0, lane);
-    oq.init(static_cast<const ET*>(g.dz) + (long)lo * g.lddz + q0, g.lddz, R, g.lddz - q0, g.N - q0, lane);
   } else {
     if (!find_block(g.offsets, g.G, g.M, BQ, qb, grp, lo, hi)) return;
     q0 = lo;
@@ -196,89 +219,116 @@ __global__ void __launch_bounds__(64 * WQ * WP) qmoe_linear(const LinearGemm g, 
       }
       return;
     }
-    if constexpr (MODE == LIN_FWD) {
-      R = g.K;
-      op.init(static_cast<const ET*>(g.w) + ((long)grp * g.N + p0) * g.ldw, g.ldw, g.N - p0, g.ldw, 0, lane);
-      oq.init(static_cast<const ET*>(g.x) + (long)lo * g.ldx, g.ldx, qrows, g.ldx, 0, lane);
-    } else {
-      R = g.N;
-      op.init(static_cast<const ET*>(g.w) + (long)grp * g.N * g.ldw + p0, g.ldw, g.N, g.ldw - p0, g.K - p0, lane);
-      oq.init(static_cast<const ET*>(g.dz) + (long)lo * g.lddz, g.lddz, qrows, g.lddz, 0, lane);
-    }
+    R = MODE == LIN_FWD ? g.K : g.N;
   }
-  const int pvalid = pcols - p0;
-  const long nk_all = (R + BK - 1) / BK;
-  const long kb = nk_all * ks_id / g.splits, ke = nk_all * (ks_id + 1) / g.splits;
-  const int nk = (int)(ke - kb);
+  // stages [kb, kb + nk) of this range
+  const int nk_all = (R + BK - 1) / BK;
+  const int kb = (int)((long)nk_all * ks_id / g.splits);
+  const int nk = (int)((long)nk_all * (ks_id + 1) / g.splits) - kb;
+  if constexpr (MODE == LIN_DW) {
+    op.init(static_cast<const ET*>(g.x) + (long)lo * g.ldx + p0, g.ldx, R, g.ldx - p0, g.K - p0, kb, wave, lane);
+    oq.init(static_cast<const ET*>(g.dz) + (long)lo * g.lddz + q0, g.lddz, R, g.lddz - q0, g.N - q0, kb, wave, lane);
+  } else if constexpr (MODE == LIN_FWD) {
+    op.init(static_cast<const ET*>(g.w) + ((long)grp * g.N + p0) * g.ldw, g.ldw, g.N - p0, g.ldw, 0, kb, wave, lane);
+    oq.init(static_cast<const ET*>(g.x) + (long)lo * g.ldx, g.ldx, qrows, g.ldx, 0, kb, wave, lane);
+  } else {
+    op.init(static_cast<const ET*>(g.w) + (long)grp * g.N * g.ldw + p0, g.ldw, g.N, g.ldw - p0, g.K - p0, kb, wave, lane);
+    oq.init(static_cast<const ET*>(g.dz) + (long)lo * g.lddz, g.lddz, qrows, g.lddz, 0, kb, wave, lane);
+  }
 
-  f32x16 acc[TP][TQ];
+  f32x4 acc[TP][TQ];
 #pragma unroll
   for (int a = 0; a < TP; ++a)
 #pragma unroll
-    for (int b = 0; b < TQ; ++b)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) acc[a][b][i] = 0.f;
+    for (int b = 0; b < TQ; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
   const int wq = wave / WP, wp = wave % WP;
 
-  auto issue = [&](int kt) {
-    char* dst = lds[kt % NST];
-    // past the range's end: nothing is in range, the loads write zeros (the
-    // count of loads in flight stays the same)
-    const long k = kt < nk ? kb + kt : nk_all + kt;
-    op.issue(dst, k, R, pvalid, wave, lane);
-    oq.issue(dst + OP::kBytes, k, R, qrows, wave, lane);
+  // stage kt into place u (= kt % NST); past the range's end zeros, so that
+  // the count of loads in flight stays the same
+  auto issue = [&](int kt, int u) {
+    op.issue(lds[u], (kb + kt) * BK, R, kt < nk, wave);
+    oq.issue(lds[u] + OP::kBytes, (kb + kt) * BK, R, kt < nk, wave);
   };
-  constexpr int kInFlight = (NST - 2) * (OP::kLoads + OQ::kLoads);
-#pragma unroll
-  for (int s = 0; s < NST - 1; ++s) issue(s);
-  for (int kt = 0; kt < nk; ++kt) {
-    // stage kt has landed (this wavefront's loads; the barrier: everyone's),
-    // and every wavefront has read stage kt - 1, whose place is filled next
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kInFlight) : "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-    issue(kt + NST - 1);
-    const char* sp = lds[kt % NST];
+  using Frag = typename LinMma<ET>::Frag;
+  struct Frags {
+    Frag p[TP], q[TQ];
+  };
+  auto read = [&](Frags& f, int u, int ks) {
+    const char* sp = lds[u];
     const char* sq = sp + OP::kBytes;
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      typename LinMma<ET>::Frag fp[TP], fq[TQ];
+    for (int a = 0; a < TP; ++a) f.p[a] = OP::frag(sp, (wp * TP + a) * 16, ks, lane);
 #pragma unroll
-      for (int a = 0; a < TP; ++a) fp[a] = OP::frag(sp, (wp * TP + a) * 32, ks, lane);
+    for (int b = 0; b < TQ; ++b) f.q[b] = OQ::frag(sq, (wq * TQ + b) * 16, ks, lane);
+  };
+  auto mma = [&](const Frags& f) {
 #pragma unroll
-      for (int b = 0; b < TQ; ++b) fq[b] = OQ::frag(sq, (wq * TQ + b) * 32, ks, lane);
+    for (int a = 0; a < TP; ++a)
 #pragma unroll
-      for (int a = 0; a < TP; ++a)
+      for (int b = 0; b < TQ; ++b) acc[a][b] = LinMma<ET>::mma(f.p[a], f.q[b], acc[a][b]);
+  };
+  // This wavefront's loads of all but the newest NST - 2 stages have landed,
+  // its LDS reads are done; then everyone's.
+  constexpr int kStage = OP::kLoads + OQ::kLoads;
+  auto meet = [&]() {
+    lin_wait<(NST - 2) * kStage>();
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+  };
+  // The operands of a k step are read from LDS while the matrix instructions
+  // of the step before run (two register sets), across stages too: when the
+  // last step's operands of a stage have been read, its place is free, so the
+  // workgroup meets there, and behind the barrier the place is filled anew
+  // (NST stages ahead) and the next stage's first operands are read.
 #pragma unroll
-        for (int b = 0; b < TQ; ++b) acc[a][b] = LinMma<ET>::mma(fp[a], fq[b], acc[a][b]);
+  for (int s = 0; s < NST - 1; ++s) issue(s, s);
+  if (nk > 0) {
+    Frags f[2];
+    meet();
+    issue(NST - 1, NST - 1);
+    read(f[0], 0, 0);
+    for (int kt = 0; kt < nk; kt += NST) {
+#pragma unroll
+      for (int u = 0; u < NST; ++u) {
+        if (kt + u >= nk) break;
+        read(f[1], u, 1);
+        mma(f[0]);
+        meet();
+        read(f[0], (u + 1) % NST, 0);
+        issue(kt + u + NST, u);
+        mma(f[1]);
+      }
     }
   }
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");  // no load outlives the workgroup
+  lin_wait<0>();  // no load outlives the workgroup
 
-  // acc[a][b][4 j + i]: column 8 j + 4 (lane / 32) + i, row lane % 32 of its
-  // 32 x 32 block.  The sums go through LDS, 32 rows of every wavefront at a
-  // time, so that output rows leave in whole runs and one copy of the epilogue
-  // serves them all; rows are padded by 16 bytes, which spreads the eight
-  // lanes of a write over the banks.
+  // acc[a][b][i]: column 4 (lane / 16) + i, row lane % 16 of its 16 x 16
+  // block.  The sums go through LDS, 32 rows of every wavefront at a time, so
+  // that output rows leave in whole runs and one copy of the epilogue serves
+  // them all; rows are padded by 16 bytes, which spreads the lanes of a write
+  // over the banks.
   constexpr int SST = BP * 4 + 16;  // bytes of a staged row
   static_assert(WQ * 32 * SST <= NST * (OP::kBytes + OQ::kBytes), "the staged rows fit the stages");
+  static_assert(TQ % 2 == 0, "two blocks of 16 rows at a time");
   char* so = lds[0];
   const long ldp = (pcols + 3) & ~3;
   const long prow0 = MODE == LIN_DW ? (long)ks_id * g.G * g.N + (long)grp * g.N : (long)ks_id * g.M;
 #pragma unroll
-  for (int b = 0; b < TQ; ++b) {
+  for (int b2 = 0; b2 < TQ / 2; ++b2) {
     __syncthreads();
 #pragma unroll
-    for (int a = 0; a < TP; ++a)
+    for (int b = 0; b < 2; ++b)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        *(f32x4*)(so + (wq * 32 + (lane & 31)) * SST + ((wp * TP + a) * 32 + 8 * j + 4 * (lane >> 5)) * 4) =
-            f32x4{acc[a][b][4 * j], acc[a][b][4 * j + 1], acc[a][b][4 * j + 2], acc[a][b][4 * j + 3]};
+      for (int a = 0; a < TP; ++a)
+        *(f32x4*)(so + (wq * 32 + b * 16 + (lane & 15)) * SST + ((wp * TP + a) * 16 + 4 * (lane >> 4)) * 4) =
+            acc[a][2 * b2 + b];
     __syncthreads();
 #pragma unroll 2
     for (int i = threadIdx.x; i < WQ * 32 * (BP / 4); i += 64 * NW) {
       const int sr = i / (BP / 4), cc = 4 * (i % (BP / 4));
-      const int qr = ((sr >> 5) * TQ + b) * 32 + (sr & 31);
+      const int qr = (sr >> 5) * (TQ * 16) + b2 * 32 + (sr & 31);
       if (qr >= qrows) continue;
       const f32x4 v = *(const f32x4*)(so + sr * SST + cc * 4);
       const int m = q0 + qr, c = p0 + cc;

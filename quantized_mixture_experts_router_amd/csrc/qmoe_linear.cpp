@@ -60,7 +60,7 @@ LinearPlan plan_product(int type, int64_t rows, int64_t groups, int64_t cols, in
       best.tile = t.tile;
       // ranges of the reduction when the tiles leave compute units idle, at
       // least eight steps each
-      best.splits = (int)std::max<int64_t>(1, std::min<int64_t>({cus * 2 / std::max<int64_t>(1, n), red / (8 * bk), 32}));
+      best.splits = (int)std::max<int64_t>(1, std::min<int64_t>({cus / std::max<int64_t>(1, n), red / (8 * bk), 32}));
     }
   }
   return best;
