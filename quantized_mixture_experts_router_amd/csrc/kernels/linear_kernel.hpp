@@ -58,7 +58,22 @@ __device__ __forceinline__ void lin_wait() {
   asm volatile("" ::: "memory");
 }
 
+// helper lambdas are always inlined (what they capture stays in registers)
+#define QMOE_INLINE __attribute__((always_inline))
 #define QMOE_LDS(p) ((__attribute__((address_space(3))) void*)(p))
+
+// 16 bytes a lane from buffer rs at vo + so into LDS at dst + 16 lane (the
+// instruction has no register output).  Written out because the compiler
+// takes every transposing LDS read for a reader of the loads in flight and
+// would wait for all of them in front of each; the waits are lin_wait's.
+__device__ __forceinline__ void load_lds16(u32x4 rs, uint32_t dst, int vo, int so) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "buffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(dst),
+      "v"(vo), "s"(rs), "s"(so)
+      : "memory", "m0");
+}
 
 // One operand's tile of BT rows or columns: fills a stage and reads fragments.
 //   RUN: rows of consecutive r.  else: r rows of consecutive columns.
@@ -114,21 +129,21 @@ struct LinOperand {
     }
   }
 
-  // The next stage into LDS at dst; r0 = its first r (of R); not on: past the
-  // range of r, nothing is read and the stage fills with zeros.
-  __device__ __forceinline__ void issue(char* dst, int r0, int R, bool on, int wave) {
+  // Load instruction i of the next stage into LDS at dst; r0 = the stage's
+  // first r (of R); not on: past the range of r, nothing is read and the
+  // stage fills with zeros.
+  __device__ __forceinline__ void load(int i, char* dst, int r0, int R, bool on, int wave) const {
     const long rem = on ? left : 0;
-    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<char*>(base), 0, (int)(rem < 0 ? 0 : rem > 0x7fffffff ? 0x7fffffff : rem), 0x00027000);
+    const int size = RUN ? max((int)rem, 0) : (int)(rem < 0 ? 0 : rem > 0x7fffffff ? 0x7fffffff : rem);
+    const uint64_t at = (uint64_t)base;
+    const u32x4 rs = {(uint32_t)at, (uint32_t)(at >> 32) & 0xffffu, (uint32_t)size, 0x00027000u};
+    const int idx = i * NW + wave;
     // the last stage: pieces from R on are out of range, not the next row
-    const int v0 = RUN && r0 + piece >= R ? kOut : voff[0];
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int idx = i * NW + wave;
-      int vo = v0;
-      if constexpr (kOffs > 1) vo = voff[i % kOffs];
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, QMOE_LDS(dst + idx * 1024), 16, vo, idx * RPI * ldb, 0, 0);
-    }
+    int vo = RUN && r0 + piece >= R ? kOut : voff[0];
+    if constexpr (kOffs > 1) vo = voff[i % kOffs];
+    load_lds16(rs, (uint32_t)(uintptr_t)QMOE_LDS(dst + idx * 1024), vo, idx * RPI * ldb);
+  }
+  __device__ __forceinline__ void next() {
     const long step = RUN ? 128 : (long)BK * ldb;
     base += step;
     left -= step;
@@ -243,62 +258,87 @@ __global__ void __launch_bounds__(64 * WQ * WP) qmoe_linear(const LinearGemm g, 
     for (int b = 0; b < TQ; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
   const int wq = wave / WP, wp = wave % WP;
 
-  // stage kt into place u (= kt % NST); past the range's end zeros, so that
-  // the count of loads in flight stays the same
-  auto issue = [&](int kt, int u) {
-    op.issue(lds[u], (kb + kt) * BK, R, kt < nk, wave);
-    oq.issue(lds[u] + OP::kBytes, (kb + kt) * BK, R, kt < nk, wave);
+  // Load instruction i of stage kt into place u (= kt % NST); past the range's
+  // end zeros, so that the count of loads in flight stays the same.
+  constexpr int kStage = OP::kLoads + OQ::kLoads;
+  auto load = [&](int i, int kt, int u) QMOE_INLINE {
+    if (i < OP::kLoads) op.load(i, lds[u], (kb + kt) * BK, R, kt < nk, wave);
+    else oq.load(i - OP::kLoads, lds[u] + OP::kBytes, (kb + kt) * BK, R, kt < nk, wave);
+    if (i == kStage - 1) {
+      op.next();
+      oq.next();
+    }
   };
   using Frag = typename LinMma<ET>::Frag;
-  struct Frags {
-    Frag p[TP], q[TQ];
-  };
-  auto read = [&](Frags& f, int u, int ks) {
-    const char* sp = lds[u];
-    const char* sq = sp + OP::kBytes;
-#pragma unroll
-    for (int a = 0; a < TP; ++a) f.p[a] = OP::frag(sp, (wp * TP + a) * 16, ks, lane);
-#pragma unroll
-    for (int b = 0; b < TQ; ++b) f.q[b] = OQ::frag(sq, (wq * TQ + b) * 16, ks, lane);
-  };
-  auto mma = [&](const Frags& f) {
-#pragma unroll
-    for (int a = 0; a < TP; ++a)
-#pragma unroll
-      for (int b = 0; b < TQ; ++b) acc[a][b] = LinMma<ET>::mma(f.p[a], f.q[b], acc[a][b]);
+  Frag fp[2][TP], fq[TQ];
+  auto read_p = [&](int a, int u, int ks) QMOE_INLINE { fp[ks][a] = OP::frag(lds[u], (wp * TP + a) * 16, ks, lane); };
+  auto read_q = [&](int b, int u, int ks) QMOE_INLINE {
+    fq[b] = OQ::frag(lds[u] + OP::kBytes, (wq * TQ + b) * 16, ks, lane);
   };
   // This wavefront's loads of all but the newest NST - 2 stages have landed,
   // its LDS reads are done; then everyone's.
-  constexpr int kStage = OP::kLoads + OQ::kLoads;
-  auto meet = [&]() {
+  auto meet = [&]() QMOE_INLINE {
     lin_wait<(NST - 2) * kStage>();
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
     asm volatile("" ::: "memory");
   };
-  // The operands of a k step are read from LDS while the matrix instructions
-  // of the step before run (two register sets), across stages too: when the
-  // last step's operands of a stage have been read, its place is free, so the
-  // workgroup meets there, and behind the barrier the place is filled anew
-  // (NST stages ahead) and the next stage's first operands are read.
+  // A stage is two k steps; a step runs its matrix instructions block by
+  // block (the TP products of one q fragment).  The next step's operands are
+  // read meanwhile: a q fragment into its own registers when its block is
+  // done, the p fragments into a second set.  In the stage's second step all
+  // of the stage has been read, so after the first blocks (which cover the
+  // last reads) the workgroup meets; behind the barrier the reads go to the
+  // next stage and this stage's place is filled anew, NST stages ahead, a few
+  // loads a block.  The scheduling barriers keep that order.
+  constexpr int kMeet = 0;  // the block behind which the workgroup meets
+  constexpr int kFill = (kStage + TQ - kMeet - 1) / (TQ - kMeet);  // loads a block behind it
+  constexpr int kPer = (TP + TQ - kMeet - 1) / (TQ - kMeet);       // p reads a block
+  auto block = [&](int b, int ks) QMOE_INLINE {
 #pragma unroll
-  for (int s = 0; s < NST - 1; ++s) issue(s, s);
+    for (int a = 0; a < TP; ++a) acc[a][b] = LinMma<ET>::mma(fp[ks][a], fq[b], acc[a][b]);
+  };
+#pragma unroll
+  for (int s = 0; s < NST - 1; ++s)
+#pragma unroll
+    for (int i = 0; i < kStage; ++i) load(i, s, s);
   if (nk > 0) {
-    Frags f[2];
     meet();
-    issue(NST - 1, NST - 1);
-    read(f[0], 0, 0);
+#pragma unroll
+    for (int i = 0; i < kStage; ++i) load(i, NST - 1, NST - 1);
+#pragma unroll
+    for (int a = 0; a < TP; ++a) read_p(a, 0, 0);
+#pragma unroll
+    for (int b = 0; b < TQ; ++b) read_q(b, 0, 0);
     for (int kt = 0; kt < nk; kt += NST) {
 #pragma unroll
       for (int u = 0; u < NST; ++u) {
         if (kt + u >= nk) break;
-        read(f[1], u, 1);
-        mma(f[0]);
-        meet();
-        read(f[0], (u + 1) % NST, 0);
-        issue(kt + u + NST, u);
-        mma(f[1]);
+#pragma unroll
+        for (int b = 0; b < TQ; ++b) {
+          block(b, 0);
+          __builtin_amdgcn_sched_barrier(0);
+          read_q(b, u, 1);
+#pragma unroll
+          for (int a = b * kPer; a < (b + 1) * kPer && a < TP; ++a) read_p(a, u, 1);
+        }
+#pragma unroll
+        for (int b = 0; b < TQ; ++b) {
+          block(b, 1);
+          __builtin_amdgcn_sched_barrier(0);
+          if (b == kMeet) meet();
+          if (b < kMeet) continue;
+          const int n = (u + 1) % NST;
+          if (b == kMeet)
+#pragma unroll
+            for (int c = 0; c < kMeet; ++c) read_q(c, n, 0);
+          read_q(b, n, 0);
+#pragma unroll
+          for (int a = (b - kMeet) * kPer; a < (b - kMeet + 1) * kPer && a < TP; ++a) read_p(a, n, 0);
+#pragma unroll
+          for (int i = (b - kMeet) * kFill; i < (b - kMeet + 1) * kFill && i < kStage; ++i) load(i, kt + u + NST, u);
+        }
       }
     }
   }
