@@ -69,7 +69,14 @@ hipError_t launch_linear_act_grad(int type, const LinearActGrad& g, hipStream_t 
 // db[g][n] = sum of the row blocks' column sums of group g, in row order.
 hipError_t launch_linear_bias_grad(int type, const float* sums, const int* offsets, int G, int M, int N, void* db,
                                    hipStream_t st);
-// rows x cols elements -> rows of ld elements, zeros from cols on.
-hipError_t launch_linear_pad(int esize, const void* src, long rows, long cols, void* dst, long ld, hipStream_t st);
+// rows x cols elements -> rows of ld elements (whole 16-byte runs, 16-byte
+// aligned), zeros from cols on; two operands (rows 0: none).
+struct LinearPad {
+  const void* src;
+  long rows, cols;
+  void* dst;
+  long ld;
+};
+hipError_t launch_linear_pad(int esize, const LinearPad& a, const LinearPad& b, hipStream_t st);
 
 }  // namespace qmoe

@@ -183,11 +183,12 @@ struct LinOperand {
   }
 };
 
-// Output tiles are taken in runs of 32 per XCD (workgroups go to the 8 XCDs in
-// turn; 32 compute units each), inside a run eight q blocks by four p blocks,
-// so that a run's operand rows are shared in its XCD's L2.
-__device__ __forceinline__ void tile_of(int b, int nq, int np, int& q, int& p) {
-  const int t = ((b >> 3) / 32 * 8 + (b & 7)) * 32 + (b >> 3) % 32;
+// Output tiles are taken in runs of up to 32 per XCD (workgroups go to the 8
+// XCDs in turn; 32 compute units each; shorter runs when there are fewer tiles
+// than compute units), inside a run eight q blocks by four p blocks, so that a
+// run's operand rows are shared in its XCD's L2.
+__device__ __forceinline__ void tile_of(int b, int run, int nq, int np, int& q, int& p) {
+  const int t = ((b >> 3) / run * 8 + (b & 7)) * run + (b >> 3) % run;
   const int h = min(nq, 8);
   const int s = t / (h * np), r = t - s * (h * np);
   q = s * h + r % h;
@@ -195,7 +196,7 @@ __device__ __forceinline__ void tile_of(int b, int nq, int np, int& q, int& p) {
 }
 
 template <typename ET, int MODE, int BQ, int BP, int WQ, int WP, int NST, bool VEC>
-__global__ void __launch_bounds__(64 * WQ * WP) qmoe_linear(const LinearGemm g, int nq, int np) {
+__global__ void __launch_bounds__(64 * WQ * WP) qmoe_linear(const LinearGemm g, int run, int nq, int np) {
   constexpr int NW = WQ * WP, TQ = BQ / WQ / 16, TP = BP / WP / 16;
   using OP = LinOperand<ET, BP, MODE == LIN_FWD, NW>;
   using OQ = LinOperand<ET, BQ, MODE != LIN_DW, NW>;
@@ -205,7 +206,7 @@ __global__ void __launch_bounds__(64 * WQ * WP) qmoe_linear(const LinearGemm g, 
 
   int qb, pb;
   const int ks_id = blockIdx.y;  // range of r
-  tile_of(blockIdx.x, nq, np, qb, pb);
+  tile_of(blockIdx.x, run, nq, np, qb, pb);
   const int p0 = pb * BP;
   int grp, lo, hi, q0, qrows;  // group, its rows from the tile on, first output row, valid rows of the tile
   const int pcols = MODE == LIN_FWD ? g.N : g.K;
@@ -393,9 +394,10 @@ hipError_t go_linear(const LinearGemm& g, bool vec, hipStream_t st) {
   const long np = (cols + BP - 1) / BP;
   const long h = nq < 8 ? nq : 8;
   const long n = (nq + h - 1) / h * h * np;  // whole runs of h q blocks
-  const dim3 grid((unsigned)((n + 255) / 256 * 256), (unsigned)g.splits), block(64 * WQ * WP);
-  if (vec) hipLaunchKernelGGL((qmoe_linear<ET, MODE, BQ, BP, WQ, WP, NST, true>), grid, block, 0, st, g, (int)nq, (int)np);
-  else hipLaunchKernelGGL((qmoe_linear<ET, MODE, BQ, BP, WQ, WP, NST, false>), grid, block, 0, st, g, (int)nq, (int)np);
+  const long run = n >= 256 ? 32 : (n + 7) / 8;
+  const dim3 grid((unsigned)((n + 8 * run - 1) / (8 * run) * (8 * run)), (unsigned)g.splits), block(64 * WQ * WP);
+  if (vec) hipLaunchKernelGGL((qmoe_linear<ET, MODE, BQ, BP, WQ, WP, NST, true>), grid, block, 0, st, g, (int)run, (int)nq, (int)np);
+  else hipLaunchKernelGGL((qmoe_linear<ET, MODE, BQ, BP, WQ, WP, NST, false>), grid, block, 0, st, g, (int)run, (int)nq, (int)np);
   return hipGetLastError();
 }
 

@@ -179,14 +179,24 @@ __global__ void __launch_bounds__(256) qmoe_linear_bias_grad(const float* __rest
   db[(long)grp * N + n] = (ET)s;
 }
 
-// cols elements of each row into rows of ld, zeros behind them: one thread an
-// element of the padded rows.
+// cols elements of each row into rows of ld (whole 16-byte pieces), zeros
+// behind them: one thread a piece, two operands a launch.
 template <typename U>
-__global__ void __launch_bounds__(256) qmoe_linear_pad(const U* __restrict__ src, long rows, int cols,
-                                                       U* __restrict__ dst, int ld) {
-  const int c = blockIdx.y * 256 + threadIdx.x;
-  if (c >= ld) return;
-  for (long r = blockIdx.x; r < rows; r += gridDim.x) dst[r * ld + c] = c < cols ? src[r * cols + c] : (U)0;
+__global__ void __launch_bounds__(256) qmoe_linear_pad(LinearPad a, LinearPad b, long pieces_a, long pieces) {
+  constexpr int N = 16 / sizeof(U);
+  typedef U V __attribute__((ext_vector_type(N)));
+  const long i = (long)blockIdx.x * 256 + threadIdx.x;
+  if (i >= pieces) return;
+  const LinearPad& t = i < pieces_a ? a : b;
+  const long j = i < pieces_a ? i : i - pieces_a;
+  const int per = (int)(t.ld / N);
+  const long r = j / per;
+  const int c = (int)(j - r * per) * N;
+  const U* src = static_cast<const U*>(t.src) + r * t.cols;
+  V v;
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] = c + k < t.cols ? src[c + k] : (U)0;
+  *(V*)(static_cast<U*>(t.dst) + r * t.ld + c) = v;
 }
 
 }  // namespace
@@ -216,14 +226,13 @@ hipError_t launch_linear_bias_grad(int type, const float* sums, const int* offse
   return hipGetLastError();
 }
 
-hipError_t launch_linear_pad(int esize, const void* src, long rows, long cols, void* dst, long ld, hipStream_t st) {
-  const dim3 grid((unsigned)(rows < 65536 ? rows : 65536), (unsigned)((ld + 255) / 256)), block(256);
-  if (esize == 4)
-    hipLaunchKernelGGL(qmoe_linear_pad<uint32_t>, grid, block, 0, st, (const uint32_t*)src, rows, (int)cols,
-                       (uint32_t*)dst, (int)ld);
-  else
-    hipLaunchKernelGGL(qmoe_linear_pad<uint16_t>, grid, block, 0, st, (const uint16_t*)src, rows, (int)cols,
-                       (uint16_t*)dst, (int)ld);
+hipError_t launch_linear_pad(int esize, const LinearPad& a, const LinearPad& b, hipStream_t st) {
+  const int n = 16 / esize;
+  const long pa = a.rows * (a.ld / n), all = pa + b.rows * (b.ld / n);
+  if (all == 0) return hipSuccess;
+  const dim3 grid((unsigned)((all + 255) / 256)), block(256);
+  if (esize == 4) hipLaunchKernelGGL(qmoe_linear_pad<uint32_t>, grid, block, 0, st, a, b, pa, all);
+  else hipLaunchKernelGGL(qmoe_linear_pad<uint16_t>, grid, block, 0, st, a, b, pa, all);
   return hipGetLastError();
 }
 

@@ -305,8 +305,8 @@ qmoe_status qmoe_linear(const qmoe_tensor* input, const qmoe_tensor* weights, co
   g.out = const_cast<void*>(output->data);
   g.pre = preact ? const_cast<void*>(preact->data) : nullptr;
   if (p.Kp != p.K) {
-    if (launch_linear_pad((int)p.es, g.x, p.M, p.K, ws + p.off_x, p.Kp, s) != hipSuccess ||
-        (wrows(p) > 0 && launch_linear_pad((int)p.es, g.w, wrows(p), p.K, ws + p.off_w, p.Kp, s) != hipSuccess))
+    if (launch_linear_pad((int)p.es, {g.x, p.M, p.K, ws + p.off_x, p.Kp}, {g.w, wrows(p), p.K, ws + p.off_w, p.Kp}, s) !=
+        hipSuccess)
       return QMOE_ERR_HIP;
     g.x = ws + p.off_x;
     g.w = ws + p.off_w;
@@ -380,9 +380,8 @@ qmoe_status qmoe_linear_backward(const qmoe_tensor* grad_output, const qmoe_tens
     return QMOE_ERR_HIP;
   float* partial = reinterpret_cast<float*>(ws + p.off_partial);
   if (p.Kp != p.K) {
-    if (gw && p.M > 0 && launch_linear_pad((int)p.es, g.x, p.M, p.K, ws + p.off_x, p.Kp, s) != hipSuccess)
-      return QMOE_ERR_HIP;
-    if (gx && wrows(p) > 0 && launch_linear_pad((int)p.es, g.w, wrows(p), p.K, ws + p.off_w, p.Kp, s) != hipSuccess)
+    if (launch_linear_pad((int)p.es, {g.x, gw ? p.M : 0, p.K, ws + p.off_x, p.Kp},
+                          {g.w, gx ? wrows(p) : 0, p.K, ws + p.off_w, p.Kp}, s) != hipSuccess)
       return QMOE_ERR_HIP;
     g.x = ws + p.off_x;
     g.w = ws + p.off_w;
