@@ -3,6 +3,8 @@
 #pragma once
 #include <math.h>
 
+#include <type_traits>
+
 #include "common.hpp"
 #include "linear.h"
 
@@ -20,10 +22,10 @@ constexpr int kActRelu = 0, kActSwiglu = 1, kActGelu = 2, kActSilu = 3, kActIden
 // reciprocal is the right 0.
 __device__ __forceinline__ float lin_sigmoid(float v) { return 1.f / (1.f + expf(-v)); }
 
-__device__ __forceinline__ float lin_act(float z, const LinearAct& a) {
-  if (a.type == kActRelu) return z < 0.f ? 0.f : z;  // NaN stays NaN
-  if (a.type == kActGelu) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
-  if (a.type == kActSilu) return z * lin_sigmoid(z);
+__device__ __forceinline__ float lin_act(float z, int act) {
+  if (act == kActRelu) return z < 0.f ? 0.f : z;  // NaN stays NaN
+  if (act == kActGelu) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+  if (act == kActSilu) return z * lin_sigmoid(z);
   return z;
 }
 
@@ -149,80 +151,111 @@ struct LinVec2 {
   typedef ET type __attribute__((ext_vector_type(2)));
 };
 
-// The epilogue of four consecutive columns n .. n + 3 of output row m: z =
-// the float32 sums, bias in, pre-activation out, activation, residual, one
-// rounding to the type.  VEC: four columns at a time (N % 4 == 0 and pointers
-// that allow it), else one by one up to N.
-template <typename ET, bool VEC>
-__device__ __forceinline__ void linear_epilogue(const LinearGemm& g, int grp, int m, int n, f32x4 z) {
-  using V4 = typename LinVec4<ET>::type;
-  using V2 = typename LinVec2<ET>::type;
-  if (n >= g.N) return;
-  const ET* bias = static_cast<const ET*>(g.bias);
+// W consecutive elements (W = 4 or 2; VEC: one access).
+template <typename ET, int W>
+struct LinVec {
+  typedef ET type __attribute__((ext_vector_type(W)));
+};
+template <typename ET, int W, bool VEC>
+__device__ __forceinline__ void load_w(const ET* p, int n, float (&v)[W]) {
   if constexpr (VEC) {
-    if (bias) {
-      const V4 b = *(const V4*)(bias + (long)grp * g.N + n);
+    const typename LinVec<ET, W>::type t = *(const typename LinVec<ET, W>::type*)p;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) z[i] += (float)b[i];
-    }
-    if (g.pre) {
-      V4 v;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = (ET)z[i];
-      *(V4*)(static_cast<ET*>(g.pre) + (long)m * g.N + n) = v;
-    }
-    if (g.act.type == kActSwiglu) {
-      const long o = (long)m * (g.N >> 1) + (n >> 1);
-      float y0 = lin_swiglu(z[0], z[1], g.act), y1 = lin_swiglu(z[2], z[3], g.act);
-      if (g.res) {
-        const V2 r = *(const V2*)(static_cast<const ET*>(g.res) + o);
-        y0 += (float)r[0];
-        y1 += (float)r[1];
-      }
-      V2 v;
-      v[0] = (ET)y0;
-      v[1] = (ET)y1;
-      *(V2*)(static_cast<ET*>(g.out) + o) = v;
-    } else {
-      const long o = (long)m * g.N + n;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) z[i] = lin_act(z[i], g.act);
-      if (g.res) {
-        const V4 r = *(const V4*)(static_cast<const ET*>(g.res) + o);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) z[i] += (float)r[i];
-      }
-      V4 v;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = (ET)z[i];
-      *(V4*)(static_cast<ET*>(g.out) + o) = v;
-    }
+    for (int i = 0; i < W; ++i) v[i] = (float)t[i];
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (n + i >= g.N) continue;
-      if (bias) z[i] += (float)bias[(long)grp * g.N + n + i];
-      if (g.pre) static_cast<ET*>(g.pre)[(long)m * g.N + n + i] = (ET)z[i];
-    }
-    if (g.act.type == kActSwiglu) {
+    for (int i = 0; i < W; ++i) v[i] = i < n ? (float)p[i] : 0.f;
+  }
+}
+template <typename ET, int W, bool VEC>
+__device__ __forceinline__ void store_w(ET* p, int n, const float (&v)[W]) {
+  if constexpr (VEC) {
+    typename LinVec<ET, W>::type t;
 #pragma unroll
-      for (int i = 0; i < 4; i += 2) {
-        if (n + i >= g.N) continue;  // N is even: both or none
-        const long o = (long)m * (g.N >> 1) + ((n + i) >> 1);
-        float y = lin_swiglu(z[i], z[i + 1], g.act);
-        if (g.res) y += (float)static_cast<const ET*>(g.res)[o];
-        static_cast<ET*>(g.out)[o] = (ET)y;
-      }
-    } else {
+    for (int i = 0; i < W; ++i) t[i] = (ET)v[i];
+    *(typename LinVec<ET, W>::type*)p = t;
+  } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (n + i >= g.N) continue;
-        const long o = (long)m * g.N + n + i;
-        float y = lin_act(z[i], g.act);
-        if (g.res) y += (float)static_cast<const ET*>(g.res)[o];
-        static_cast<ET*>(g.out)[o] = (ET)y;
-      }
+    for (int i = 0; i < W; ++i)
+      if (i < n) p[i] = (ET)v[i];
+  }
+}
+
+// The epilogue of W consecutive columns c .. of R output rows m[r] (those with
+// ok[r]), the columns' biases in b: z = the float32 sums + bias,
+// pre-activation out, activation, residual, one rounding to the type.  VEC: a
+// row's columns in one access (N % 4 == 0 and pointers that allow it), else
+// one by one up to N.  The rows go through each step together, so that their
+// accesses overlap.
+template <typename ET, int ACT, int W, int R, bool VEC>
+__device__ __forceinline__ void linear_rows(const LinearGemm& g, float (&z)[R][W], const float (&b)[W], int c,
+                                            const int (&m)[R], const bool (&ok)[R]) {
+  const int n = g.N - c;
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int i = 0; i < W; ++i) z[r][i] += b[i];
+  if (g.pre) {
+    ET* pre = static_cast<ET*>(g.pre) + c;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (ok[r]) store_w<ET, W, VEC>(pre + (long)m[r] * g.N, n, z[r]);
+  }
+  if constexpr (ACT == kActSwiglu) {
+    constexpr int H = W / 2;
+    const long No = g.N >> 1;
+    float y[R][H];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int i = 0; i < H; ++i) y[r][i] = lin_swiglu(z[r][2 * i], z[r][2 * i + 1], g.act);
+    if (g.res) {
+      const ET* res = static_cast<const ET*>(g.res) + (c >> 1);
+      float v[R][H];
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (ok[r]) load_w<ET, H, VEC>(res + m[r] * No, n >> 1, v[r]);
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int i = 0; i < H; ++i) y[r][i] += v[r][i];
     }
+    ET* out = static_cast<ET*>(g.out) + (c >> 1);
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (ok[r]) store_w<ET, H, VEC>(out + m[r] * No, n >> 1, y[r]);
+  } else {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int i = 0; i < W; ++i) z[r][i] = lin_act(z[r][i], ACT);
+    if (g.res) {
+      const ET* res = static_cast<const ET*>(g.res) + c;
+      float v[R][W];
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (ok[r]) load_w<ET, W, VEC>(res + (long)m[r] * g.N, n, v[r]);
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int i = 0; i < W; ++i) z[r][i] += v[r][i];
+    }
+    ET* out = static_cast<ET*>(g.out) + c;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (ok[r]) store_w<ET, W, VEC>(out + (long)m[r] * g.N, n, z[r]);
+  }
+}
+
+// f(ACT) with the activation as a compile-time constant.
+template <typename F>
+__device__ __forceinline__ void with_act(int act, F f) {
+  switch (act) {
+    case kActRelu: f(std::integral_constant<int, kActRelu>{}); break;
+    case kActSwiglu: f(std::integral_constant<int, kActSwiglu>{}); break;
+    case kActGelu: f(std::integral_constant<int, kActGelu>{}); break;
+    case kActSilu: f(std::integral_constant<int, kActSilu>{}); break;
+    default: f(std::integral_constant<int, kActIdentity>{});
   }
 }
 

@@ -278,12 +278,15 @@ __global__ void __launch_bounds__(64 * WQ * WP) qmoe_linear(const LinearGemm g, 
   };
   // This wavefront's loads of all but the newest NST - 2 stages have landed,
   // its LDS reads are done; then everyone's.
-  auto meet = [&]() QMOE_INLINE {
-    lin_wait<(NST - 2) * kStage>();
+  auto barrier = [&]() QMOE_INLINE {
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
     asm volatile("" ::: "memory");
+  };
+  auto meet = [&]() QMOE_INLINE {
+    lin_wait<(NST - 2) * kStage>();
+    barrier();
   };
   // A stage is two k steps; a step runs its matrix instructions block by
   // block (the TP products of one q fragment).  The next step's operands are
@@ -349,39 +352,78 @@ __global__ void __launch_bounds__(64 * WQ * WP) qmoe_linear(const LinearGemm g, 
   // block.  The sums go through LDS, 32 rows of every wavefront at a time, so
   // that output rows leave in whole runs and one copy of the epilogue serves
   // them all; rows are padded by 16 bytes, which spreads the lanes of a write
-  // over the banks.
+  // over the banks.  The barriers wait for LDS accesses alone: waiting for the
+  // output's stores too, as __syncthreads does, took 19 us a tile (4096 x 1536
+  // -> 4096 outputs).
   constexpr int SST = BP * 4 + 16;  // bytes of a staged row
   static_assert(WQ * 32 * SST <= NST * (OP::kBytes + OQ::kBytes), "the staged rows fit the stages");
   static_assert(TQ % 2 == 0, "two blocks of 16 rows at a time");
   char* so = lds[0];
   const long ldp = (pcols + 3) & ~3;
   const long prow0 = MODE == LIN_DW ? (long)ks_id * g.G * g.N + (long)grp * g.N : (long)ks_id * g.M;
-#pragma unroll
+  // A thread keeps its W columns over all rows; RS rows of a step go together.
+  constexpr int W = VEC ? 4 : 2, TPR = BP / W, RPS = 64 * NW / TPR, RS = 4;
+  static_assert(WQ * 32 % (RPS * RS) == 0, "whole steps of rows");
+  const int cc = (threadIdx.x % TPR) * W, c = p0 + cc, r0 = threadIdx.x / TPR;
+  const bool inside = c < pcols;
+  float bias[W] = {};
+  if constexpr (MODE == LIN_FWD) {
+    if (g.bias && inside && g.splits == 1)
+      load_w<ET, W, VEC>(static_cast<const ET*>(g.bias) + (long)grp * g.N + c, g.N - c, bias);
+  }
   for (int b2 = 0; b2 < TQ / 2; ++b2) {
-    __syncthreads();
+    lin_wait<63>();
+    barrier();
+    // (one copy of the code behind this for all blocks)
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
+    for (int k = 0; k < TQ / 2; ++k)
+      if (k == b2)
 #pragma unroll
-      for (int a = 0; a < TP; ++a)
-        *(f32x4*)(so + (wq * 32 + b * 16 + (lane & 15)) * SST + ((wp * TP + a) * 16 + 4 * (lane >> 4)) * 4) =
-            acc[a][2 * b2 + b];
-    __syncthreads();
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int a = 0; a < TP; ++a)
+            *(f32x4*)(so + (wq * 32 + b * 16 + (lane & 15)) * SST + ((wp * TP + a) * 16 + 4 * (lane >> 4)) * 4) =
+                acc[a][2 * k + b];
+    lin_wait<63>();
+    barrier();
+    if (g.splits > 1) {
 #pragma unroll 2
-    for (int i = threadIdx.x; i < WQ * 32 * (BP / 4); i += 64 * NW) {
-      const int sr = i / (BP / 4), cc = 4 * (i % (BP / 4));
-      const int qr = (sr >> 5) * (TQ * 16) + b2 * 32 + (sr & 31);
-      if (qr >= qrows) continue;
-      const f32x4 v = *(const f32x4*)(so + sr * SST + cc * 4);
-      const int m = q0 + qr, c = p0 + cc;
-      if (g.splits > 1) {
-        if (c < ldp) *(f32x4*)(g.partial + (prow0 + m) * ldp + c) = v;
-      } else if constexpr (MODE == LIN_FWD) {
-        linear_epilogue<ET, VEC>(g, grp, m, c, v);
-      } else {
-        ET* row = static_cast<ET*>(g.out) + (MODE == LIN_DW ? ((long)grp * g.N + m) * g.K : (long)m * g.K);
-        store_cols4<ET, VEC>(row, c, g.K, v);
+      for (int i = threadIdx.x; i < WQ * 32 * (BP / 4); i += 64 * NW) {
+        const int sr = i / (BP / 4), c4 = 4 * (i % (BP / 4));
+        const int qr = (sr >> 5) * (TQ * 16) + b2 * 32 + (sr & 31);
+        if (qr < qrows && p0 + c4 < ldp)
+          *(f32x4*)(g.partial + (prow0 + q0 + qr) * ldp + p0 + c4) = *(const f32x4*)(so + sr * SST + c4 * 4);
       }
+      continue;
     }
+    if (!inside) continue;
+    auto rows = [&](auto act) QMOE_INLINE {
+      for (int s0 = 0; s0 < WQ * 32; s0 += RPS * RS) {
+        float z[RS][W];
+        int m[RS];
+        bool ok[RS];
+#pragma unroll
+        for (int r = 0; r < RS; ++r) {
+          const int sr = s0 + r * RPS + r0;
+          const int qr = (sr >> 5) * (TQ * 16) + b2 * 32 + (sr & 31);
+          ok[r] = qr < qrows;
+          m[r] = q0 + qr;
+          const typename LinVec<float, W>::type v = *(const typename LinVec<float, W>::type*)(so + sr * SST + cc * 4);
+#pragma unroll
+          for (int i = 0; i < W; ++i) z[r][i] = v[i];
+        }
+        if constexpr (MODE == LIN_FWD) {
+          linear_rows<ET, decltype(act)::value, W, RS, VEC>(g, z, bias, c, m, ok);
+        } else {
+          ET* out = static_cast<ET*>(g.out) + (MODE == LIN_DW ? (long)grp * g.N * g.K : 0) + c;
+#pragma unroll
+          for (int r = 0; r < RS; ++r)
+            if (ok[r]) store_w<ET, W, VEC>(out + (long)m[r] * g.K, g.K - c, z[r]);
+        }
+      }
+    };
+    if constexpr (MODE == LIN_FWD) with_act(g.act.type, rows);
+    else rows(std::integral_constant<int, kActIdentity>{});
   }
 }
 

@@ -44,8 +44,14 @@ __global__ void __launch_bounds__(256) qmoe_linear_finish(const LinearGemm g) {
   }
   f32x4 v = {0.f, 0.f, 0.f, 0.f};
   for (int s = 0; s < g.splits; ++s) v += *(const f32x4*)(g.partial + (s * rows + row) * ldp + c);
-  if constexpr (MODE == LIN_FWD) linear_epilogue<ET, VEC>(g, grp, (int)row, c, v);
-  else store_cols4<ET, VEC>(static_cast<ET*>(g.out) + row * g.K, c, g.K, v);
+  if constexpr (MODE == LIN_FWD) {
+    float z[1][4] = {{v[0], v[1], v[2], v[3]}}, b[4] = {};
+    const int m[1] = {(int)row};
+    const bool ok[1] = {true};
+    if (c >= g.N) return;
+    if (g.bias) load_w<ET, 4, VEC>(static_cast<const ET*>(g.bias) + (long)grp * g.N + c, g.N - c, b);
+    with_act(g.act.type, [&](auto act) { linear_rows<ET, decltype(act)::value, 4, 1, VEC>(g, z, b, c, m, ok); });
+  } else store_cols4<ET, VEC>(static_cast<ET*>(g.out) + row * g.K, c, g.K, v);
 }
 
 template <typename ET, int MODE>
