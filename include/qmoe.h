@@ -475,7 +475,7 @@ qmoe_status qmoe_route_backward(const qmoe_tensor* grad_weights, const qmoe_tens
  * takes a row behind the last expert's (in slot order), which is zero, and
  * inverse holds -1 - row.  experts <= 1023, T * k < 2^30
  * (QMOE_ERR_UNSUPPORTED).  workspace: qmoe_dispatch_workspace_size bytes,
- * 256-byte aligned (NULL when 0: up to 4096 slots need none). */
+ * 256-byte aligned (NULL when 0: up to 16384 slots need none). */
 qmoe_status qmoe_dispatch_workspace_size(const qmoe_tensor* input, const qmoe_tensor* indices, int64_t experts,
                                          size_t* bytes);
 qmoe_status qmoe_dispatch(const qmoe_tensor* input, const qmoe_tensor* indices, int64_t experts,

@@ -25,8 +25,11 @@ no fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
+import struct
+import threading
 from typing import Optional
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -138,17 +141,18 @@ def _lib():
         LA, I32, I64, P, Z = (ctypes.POINTER(QmoeLinearAttrs), ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p,
                               ctypes.c_size_t)
         ZP = ctypes.POINTER(ctypes.c_size_t)
-        for name, args in (("qmoe_route", [T, I32, I32, I32, T, T, P]),
-                           ("qmoe_route_backward", [T, T, T, I32, I32, T, P]),
-                           ("qmoe_dispatch_workspace_size", [T, T, I64, ZP]),
-                           ("qmoe_dispatch", [T, T, I64, T, T, T, T, P, Z, P]),
-                           ("qmoe_dispatch_backward", [T, T, T, P]),
-                           ("qmoe_combine", [T, T, T, T, P]),
-                           ("qmoe_combine_backward", [T] * 6 + [P]),
-                           ("qmoe_linear_workspace_size", [T] * 5 + [LA, T, T, ZP]),
-                           ("qmoe_linear", [T] * 5 + [LA, T, T, P, Z, P]),
-                           ("qmoe_linear_backward_workspace_size", [T] * 5 + [LA, T, T, T, ZP]),
-                           ("qmoe_linear_backward", [T] * 5 + [LA, T, T, T, P, Z, P])):
+        D = P  # tensors as addresses into the packed arguments (_pack)
+        for name, args in (("qmoe_route", [D, I32, I32, I32, D, D, P]),
+                           ("qmoe_route_backward", [D, D, D, I32, I32, D, P]),
+                           ("qmoe_dispatch_workspace_size", [D, D, I64, ZP]),
+                           ("qmoe_dispatch", [D, D, I64, D, D, D, D, P, Z, P]),
+                           ("qmoe_dispatch_backward", [D, D, D, P]),
+                           ("qmoe_combine", [D, D, D, D, P]),
+                           ("qmoe_combine_backward", [D] * 6 + [P]),
+                           ("qmoe_linear_workspace_size", [D] * 5 + [LA, D, D, ZP]),
+                           ("qmoe_linear", [D] * 5 + [LA, D, D, P, Z, P]),
+                           ("qmoe_linear_backward_workspace_size", [D] * 5 + [LA, D, D, D, ZP]),
+                           ("qmoe_linear_backward", [D] * 5 + [LA, D, D, D, P, Z, P])):
             getattr(lib, name).argtypes = args
             getattr(lib, name).restype = ctypes.c_int
         lib.qmoe_linear_attrs_default.argtypes = [LA]
@@ -473,32 +477,89 @@ def moe_forward(tensors: dict, attrs=None, stream=None, workspace=None, output=N
 
 
 # ------------------------------------------------------------------ steps of a routed layer
-class _on:
-    """The device of a call's tensors made current, and ``stream`` (or that
-    device's current stream) torch's stream, so that what torch allocates
-    belongs to the stream the work runs on.  All tensors lie on one device."""
+# These calls are small next to their launches, so their arguments are packed
+# at once: every tensor's qmoe_tensor lies in one buffer per thread, which the
+# library reads during the call only.
+_FMT = [struct.Struct("=" + "qiiqqq" * n) for n in range(12)]
+_CODES = {"float32": QMOE_F32, "uint8": QMOE_U8, "int32": QMOE_I32, "int64": QMOE_I64, "float16": QMOE_F16,
+          "bfloat16": QMOE_BF16, "float64": QMOE_F64}
+_code_of = {}  # torch dtype -> code, filled as types are met
+_tls = threading.local()
 
-    def __init__(self, stream, tensors):
+
+def _pack(ts):
+    """Addresses (None for None) of the tensors' descriptors in this thread's
+    buffer, valid until its next _pack."""
+    buf = getattr(_tls, "buf", None)
+    if buf is None:
+        buf = _tls.buf = ctypes.create_string_buffer(40 * len(_FMT))
+        _tls.at = ctypes.addressof(buf)
+    vals, out, at = [], [], _tls.at
+    for t in ts:
+        if t is None:
+            vals += (0, 0, 0, 0, 0, 0)
+            out.append(None)
+        else:
+            dt = t.dtype
+            code = _code_of.get(dt)
+            if code is None:
+                code = _code_of[dt] = _CODES.get(str(dt).replace("torch.", ""), 0)
+            shape = t.shape
+            r = len(shape)
+            ptr = 0
+            if hasattr(t, "data_ptr"):
+                if not t.is_contiguous():
+                    raise ValueError("qmoe tensors must be contiguous")
+                ptr = t.data_ptr()
+            if r == 2:
+                vals += (ptr, code, 2, shape[0], shape[1], 0)
+            else:
+                d = tuple(shape[:3]) + (0, 0, 0)
+                vals += (ptr, code, r, d[0], d[1], d[2])
+            out.append(at)
+        at += 40
+    _FMT[len(ts)].pack_into(buf, 0, *vals)
+    return out
+
+
+class _Stream:
+    """The device of a call's tensors made current, and ``stream`` torch's
+    stream, so that what torch allocates belongs to the stream that the work
+    runs on."""
+
+    def __init__(self, device, stream):
         import torch
-        devices = {t.device for t in tensors if t is not None}
-        if len(devices) != 1 or next(iter(devices)).type != "cuda":
-            raise ValueError(f"qmoe tensors must be on one GPU, got {sorted(map(str, devices))}")
-        self.device = next(iter(devices))
-        if stream is not None and stream.device != self.device:
-            raise ValueError(f"stream of {stream.device}, tensors on {self.device}")
-        same = self.device.index == torch.cuda.current_device()
-        self.enter = ([] if same else [torch.cuda.device(self.device)]) + \
-            ([] if stream is None else [torch.cuda.stream(stream)])
+        self.ctx = [torch.cuda.device(device)] + ([] if stream is None else [torch.cuda.stream(stream)])
 
     def __enter__(self):
-        import torch
-        for c in self.enter:
+        for c in self.ctx:
             c.__enter__()
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
 
     def __exit__(self, *exc):
-        for c in reversed(self.enter):
+        for c in reversed(self.ctx):
             c.__exit__(*exc)
+
+
+_NOTHING = contextlib.nullcontext()
+
+
+def _on(stream, ts):
+    """(context, stream handle) of a call on these tensors, which lie on one
+    GPU: its current stream unless ``stream`` is given."""
+    import torch
+    dev = None
+    for t in ts:
+        if t is not None:
+            d = t.get_device()
+            if dev is None:
+                dev = d
+            if d != dev or d < 0:
+                raise ValueError("qmoe tensors must be on one GPU, got "
+                                 f"{sorted({str(u.device) for u in ts if u is not None})}")
+    if stream is not None and stream.device.index != dev:
+        raise ValueError(f"stream of {stream.device}, tensors on cuda:{dev}")
+    ctx = _NOTHING if stream is None and dev == torch.cuda.current_device() else _Stream(dev, stream)
+    return ctx, (torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream
 
 
 def _ok(status, where):
@@ -506,18 +567,26 @@ def _ok(status, where):
         raise QmoeError(status, where)
 
 
-def _workspace(workspace, need, device):
-    """(pointer, bytes, tensor kept alive for the call) of a workspace of ``need`` bytes."""
-    import torch
-    if need == 0:
-        return None, 0, None
+def _ws(workspace, need, like):
+    """(pointer, bytes, tensor to keep until the call is enqueued) of a workspace of ``need`` bytes."""
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        if need == 0:
+            return None, 0, None
+        workspace = like.new_empty(need, dtype=_uint8())
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
+def _uint8():
+    import torch
+    return torch.uint8
+
+
 def _route_args(attrs):
-    a = attrs if isinstance(attrs, QmoeAttrs) else make_attrs(attrs)
+    if isinstance(attrs, dict):
+        r = attrs.get("routing", "qmoe")
+        return (attrs.get("k", 1), QMOE_ROUTING.get(r, 99) if isinstance(r, str) else r,
+                attrs.get("normalize_routing_weights", 0))
+    a = make_attrs() if attrs is None else attrs
     return a.k, a.routing, a.normalize_routing_weights
 
 
@@ -525,137 +594,128 @@ def qmoe_route(router_probs, attrs, indices, weights, stream=None) -> None:
     """Enqueue the routing weights: ``attrs`` holds k, routing and
     normalize_routing_weights (those of ``forward``); indices int32 and
     weights float32, both [T, k]."""
-    k, routing, norm = _route_args(attrs)
-    with _on(stream, (router_probs, indices, weights)) as st:
-        _ok(_lib().qmoe_route(_ref(router_probs, True), k, routing, norm, _ref(indices, True), _ref(weights, True), st),
-            "qmoe_route")
+    route(router_probs, attrs, stream, indices, weights)
 
 
 def route(router_probs, attrs=None, stream=None, indices=None, weights=None):
     """Allocate what is not given, then qmoe_route: (indices, weights)."""
     import torch
     k, routing, norm = _route_args(attrs)
-    with _on(stream, (router_probs, indices, weights)) as st:
-        shape = (router_probs.shape[0], max(int(k), 0))
+    ctx, st = _on(stream, (router_probs, indices, weights))
+    with ctx:
         if indices is None:
-            indices = torch.empty(shape, dtype=torch.int32, device=router_probs.device)
+            indices = router_probs.new_empty((router_probs.shape[0], max(int(k), 0)), dtype=torch.int32)
         if weights is None:
-            weights = torch.empty(shape, dtype=torch.float32, device=router_probs.device)
-        _ok(_lib().qmoe_route(_ref(router_probs, True), k, routing, norm, _ref(indices, True), _ref(weights, True), st),
-            "qmoe_route")
+            weights = router_probs.new_empty(indices.shape, dtype=torch.float32)
+        p, i, w = _pack((router_probs, indices, weights))
+        _ok(_lib().qmoe_route(p, k, routing, norm, i, w, st), "qmoe_route")
     return indices, weights
 
 
 def qmoe_route_backward(grad_weights, router_probs, indices, attrs, grad_router_probs, stream=None) -> None:
     """Enqueue the gradient of qmoe_route at the logits (attrs: routing and
     normalize_routing_weights; k is indices' second extent)."""
-    _, routing, norm = _route_args(attrs)
-    with _on(stream, (grad_weights, router_probs, indices, grad_router_probs)) as st:
-        _ok(_lib().qmoe_route_backward(_ref(grad_weights, True), _ref(router_probs, True), _ref(indices, True),
-                                       routing, norm, _ref(grad_router_probs, True), st), "qmoe_route_backward")
+    route_backward(grad_weights, router_probs, indices, attrs, stream, grad_router_probs)
 
 
 def route_backward(grad_weights, router_probs, indices, attrs=None, stream=None, grad_router_probs=None):
     """Allocate grad_router_probs [T, E] unless given, then qmoe_route_backward."""
     import torch
     _, routing, norm = _route_args(attrs)
-    with _on(stream, (grad_weights, router_probs, indices, grad_router_probs)) as st:
+    ctx, st = _on(stream, (grad_weights, router_probs, indices, grad_router_probs))
+    with ctx:
         if grad_router_probs is None:
             grad_router_probs = torch.empty_like(router_probs)
-        _ok(_lib().qmoe_route_backward(_ref(grad_weights, True), _ref(router_probs, True), _ref(indices, True),
-                                       routing, norm, _ref(grad_router_probs, True), st), "qmoe_route_backward")
+        g, p, i, o = _pack((grad_weights, router_probs, indices, grad_router_probs))
+        _ok(_lib().qmoe_route_backward(g, p, i, routing, norm, o, st), "qmoe_route_backward")
     return grad_router_probs
 
 
 def qmoe_dispatch_workspace_size(input, indices, experts) -> int:
     """Workspace bytes of qmoe_dispatch.  Arrays may live anywhere."""
     n = ctypes.c_size_t(0)
-    _ok(_lib().qmoe_dispatch_workspace_size(_ref(input, False), _ref(indices, False), int(experts), ctypes.byref(n)),
+    _ok(_lib().qmoe_dispatch_workspace_size(*_refs(input, indices), int(experts), ctypes.byref(n)),
         "qmoe_dispatch_workspace_size")
-    return int(n.value)
+    return n.value
 
 
 def qmoe_dispatch(input, indices, experts, rows, offsets, perm, inverse, workspace=None, stream=None) -> None:
     """Enqueue the sort of the slots by expert and the copy of their tokens'
     rows; ``perm`` may be None, ``workspace`` too when its size is 0."""
-    with _on(stream, (input, indices, rows, offsets, perm, inverse, workspace)) as st:
-        p, n, _keep = _workspace(workspace, 0 if workspace is None else 1, input.device)
-        _ok(_lib().qmoe_dispatch(_ref(input, True), _ref(indices, True), int(experts), _ref(rows, True),
-                                 _ref(offsets, True), _ref(perm, True), _ref(inverse, True), p, n, st),
-            "qmoe_dispatch")
+    ctx, st = _on(stream, (input, indices, rows, offsets, perm, inverse, workspace))
+    with ctx:
+        w, n, _keep = _ws(workspace, 0, input)
+        x, i, r, o, p, v = _pack((input, indices, rows, offsets, perm, inverse))
+        _ok(_lib().qmoe_dispatch(x, i, int(experts), r, o, p, v, w, n, st), "qmoe_dispatch")
 
 
 def dispatch(input, indices, experts, stream=None, workspace=None):
     """Allocate and qmoe_dispatch: (rows [T k, H], offsets [experts + 1], perm [T k], inverse [T, k])."""
     import torch
-    with _on(stream, (input, indices, workspace)) as st:
-        need = qmoe_dispatch_workspace_size(input, indices, experts)
-        dev = input.device
+    ctx, st = _on(stream, (input, indices, workspace))
+    with ctx:
+        lib = _lib()
+        need = ctypes.c_size_t(0)
+        x, i = _pack((input, indices))
+        _ok(lib.qmoe_dispatch_workspace_size(x, i, int(experts), ctypes.byref(need)), "qmoe_dispatch_workspace_size")
         T, k = indices.shape
-        rows = torch.empty((T * k, input.shape[1]), dtype=input.dtype, device=dev)
-        offsets = torch.empty(experts + 1, dtype=torch.int32, device=dev)
-        perm = torch.empty(T * k, dtype=torch.int32, device=dev)
-        inverse = torch.empty((T, k), dtype=torch.int32, device=dev)
-        p, n, _keep = _workspace(workspace, need, dev)
-        _ok(_lib().qmoe_dispatch(_ref(input, True), _ref(indices, True), int(experts), _ref(rows, True),
-                                 _ref(offsets, True), _ref(perm, True), _ref(inverse, True), p, n, st),
-            "qmoe_dispatch")
+        rows = input.new_empty((T * k, input.shape[1]))
+        offsets = indices.new_empty(experts + 1, dtype=torch.int32)
+        perm = indices.new_empty(T * k, dtype=torch.int32)
+        inverse = indices.new_empty((T, k), dtype=torch.int32)
+        w, n, _keep = _ws(workspace, need.value, input)
+        x, i, r, o, p, v = _pack((input, indices, rows, offsets, perm, inverse))
+        _ok(lib.qmoe_dispatch(x, i, int(experts), r, o, p, v, w, n, st), "qmoe_dispatch")
     return rows, offsets, perm, inverse
 
 
 def qmoe_dispatch_backward(grad_rows, inverse, grad_input, stream=None) -> None:
     """Enqueue the gradient of qmoe_dispatch at its input."""
-    with _on(stream, (grad_rows, inverse, grad_input)) as st:
-        _ok(_lib().qmoe_dispatch_backward(_ref(grad_rows, True), _ref(inverse, True), _ref(grad_input, True), st),
-            "qmoe_dispatch_backward")
+    dispatch_backward(grad_rows, inverse, stream, grad_input)
 
 
 def dispatch_backward(grad_rows, inverse, stream=None, grad_input=None):
     """Allocate grad_input [T, H] unless given, then qmoe_dispatch_backward."""
-    import torch
-    with _on(stream, (grad_rows, inverse, grad_input)) as st:
+    ctx, st = _on(stream, (grad_rows, inverse, grad_input))
+    with ctx:
         if grad_input is None:
-            grad_input = torch.empty((inverse.shape[0], grad_rows.shape[1]), dtype=grad_rows.dtype,
-                                     device=grad_rows.device)
-        _ok(_lib().qmoe_dispatch_backward(_ref(grad_rows, True), _ref(inverse, True), _ref(grad_input, True), st),
-            "qmoe_dispatch_backward")
+            grad_input = grad_rows.new_empty((inverse.shape[0], grad_rows.shape[1]))
+        g, v, o = _pack((grad_rows, inverse, grad_input))
+        _ok(_lib().qmoe_dispatch_backward(g, v, o, st), "qmoe_dispatch_backward")
     return grad_input
 
 
 def qmoe_combine(rows, inverse, weights, output, stream=None) -> None:
     """Enqueue the weighted sum of each token's rows (weights None: 1)."""
-    with _on(stream, (rows, inverse, weights, output)) as st:
-        _ok(_lib().qmoe_combine(_ref(rows, True), _ref(inverse, True), _ref(weights, True), _ref(output, True), st),
-            "qmoe_combine")
+    combine(rows, inverse, weights, stream, output)
 
 
 def combine(rows, inverse, weights=None, stream=None, output=None):
     """Allocate output [T, H] unless given, then qmoe_combine."""
-    import torch
-    with _on(stream, (rows, inverse, weights, output)) as st:
+    ctx, st = _on(stream, (rows, inverse, weights, output))
+    with ctx:
         if output is None:
-            output = torch.empty((inverse.shape[0], rows.shape[1]), dtype=rows.dtype, device=rows.device)
-        _ok(_lib().qmoe_combine(_ref(rows, True), _ref(inverse, True), _ref(weights, True), _ref(output, True), st),
-            "qmoe_combine")
+            output = rows.new_empty((inverse.shape[0], rows.shape[1]))
+        r, v, w, o = _pack((rows, inverse, weights, output))
+        _ok(_lib().qmoe_combine(r, v, w, o, st), "qmoe_combine")
     return output
 
 
 def qmoe_combine_backward(grad_output, rows, inverse, weights, grad_rows, grad_weights, stream=None) -> None:
     """Enqueue the gradients of qmoe_combine (either may be None)."""
-    with _on(stream, (grad_output, rows, inverse, weights, grad_rows, grad_weights)) as st:
-        _ok(_lib().qmoe_combine_backward(_ref(grad_output, True), _ref(rows, True), _ref(inverse, True),
-                                         _ref(weights, True), _ref(grad_rows, True), _ref(grad_weights, True), st),
+    ctx, st = _on(stream, (grad_output, rows, inverse, weights, grad_rows, grad_weights))
+    with ctx:
+        _ok(_lib().qmoe_combine_backward(*_pack((grad_output, rows, inverse, weights, grad_rows, grad_weights)), st),
             "qmoe_combine_backward")
 
 
 def combine_backward(grad_output, rows, inverse, weights, stream=None):
     """Allocate and qmoe_combine_backward: (grad_rows, grad_weights)."""
     import torch
-    with _on(stream, (grad_output, rows, inverse, weights)) as st:
-        grad_rows = torch.empty_like(rows)
-        grad_weights = torch.empty_like(weights)
-        _ok(_lib().qmoe_combine_backward(_ref(grad_output, True), _ref(rows, True), _ref(inverse, True),
-                                         _ref(weights, True), _ref(grad_rows, True), _ref(grad_weights, True), st),
+    ctx, st = _on(stream, (grad_output, rows, inverse, weights))
+    with ctx:
+        grad_rows, grad_weights = torch.empty_like(rows), torch.empty_like(weights)
+        _ok(_lib().qmoe_combine_backward(*_pack((grad_output, rows, inverse, weights, grad_rows, grad_weights)), st),
             "qmoe_combine_backward")
     return grad_rows, grad_weights
 
@@ -669,9 +729,9 @@ def qmoe_linear_attrs_default() -> QmoeLinearAttrs:
 
 def make_linear_attrs(attrs: Optional[dict] = None) -> QmoeLinearAttrs:
     """qmoe_linear_attrs from a dict of the float MoE's attribute names."""
-    a = qmoe_linear_attrs_default()
+    a = QmoeLinearAttrs(QMOE_ACT["identity"], 0, 1.0, 0.0, 0, 0.0)  # qmoe_linear_attrs_default
     for key, val in (attrs or {}).items():
-        if key not in {f[0] for f in QmoeLinearAttrs._fields_}:
+        if key not in _LINEAR_ATTRS:
             raise ValueError(f"no attribute {key!r} of a linear layer")
         if key == "activation_type" and isinstance(val, str):
             val = QMOE_ACT.get(val, 99)
@@ -682,18 +742,24 @@ def make_linear_attrs(attrs: Optional[dict] = None) -> QmoeLinearAttrs:
     return a
 
 
+_LINEAR_ATTRS = frozenset(f[0] for f in QmoeLinearAttrs._fields_)
+
+
 def _linear_a(attrs):
     return attrs if isinstance(attrs, QmoeLinearAttrs) else make_linear_attrs(attrs)
+
+
+def _refs(*ts):
+    return [_ref(t, False) for t in ts]
 
 
 def qmoe_linear_workspace_size(input, weights, bias=None, residual=None, offsets=None, attrs=None, output=None,
                                preact=None) -> int:
     """Workspace bytes of qmoe_linear.  Arrays may live anywhere."""
     a, n = _linear_a(attrs), ctypes.c_size_t(0)
-    _ok(_lib().qmoe_linear_workspace_size(*[_ref(t, False) for t in (input, weights, bias, residual, offsets)],
-                                          ctypes.byref(a), _ref(output, False), _ref(preact, False), ctypes.byref(n)),
-        "qmoe_linear_workspace_size")
-    return int(n.value)
+    _ok(_lib().qmoe_linear_workspace_size(*_refs(input, weights, bias, residual, offsets), ctypes.byref(a),
+                                          *_refs(output, preact), ctypes.byref(n)), "qmoe_linear_workspace_size")
+    return n.value
 
 
 def qmoe_linear(input, weights, bias, residual, offsets, attrs, output, preact=None, workspace=None,
@@ -702,28 +768,29 @@ def qmoe_linear(input, weights, bias, residual, offsets, attrs, output, preact=N
     offsets [G + 1]; bias, residual and preact may be None, workspace too when
     its size is 0."""
     a = _linear_a(attrs)
-    with _on(stream, (input, weights, bias, residual, offsets, output, preact, workspace)) as st:
-        p, n, _keep = _workspace(workspace, 0 if workspace is None else 1, input.device)
-        _ok(_lib().qmoe_linear(*[_ref(t, True) for t in (input, weights, bias, residual, offsets)], ctypes.byref(a),
-                               _ref(output, True), _ref(preact, True), p, n, st), "qmoe_linear")
+    ctx, st = _on(stream, (input, weights, bias, residual, offsets, output, preact, workspace))
+    with ctx:
+        w, n, _keep = _ws(workspace, 0, input)
+        t = _pack((input, weights, bias, residual, offsets, output, preact))
+        _ok(_lib().qmoe_linear(*t[:5], ctypes.byref(a), t[5], t[6], w, n, st), "qmoe_linear")
 
 
 def linear(input, weights, bias=None, residual=None, offsets=None, attrs=None, keep_preact=False, stream=None,
            workspace=None, output=None):
     """Allocate output (and preact with ``keep_preact``), then qmoe_linear:
     output, or (output, preact)."""
-    import torch
     a = _linear_a(attrs)
-    with _on(stream, (input, weights, bias, residual, offsets, workspace, output)) as st:
+    ctx, st = _on(stream, (input, weights, bias, residual, offsets, workspace, output))
+    with ctx:
         M, N = input.shape[0], weights.shape[-2]
-        No = N // 2 if a.activation_type == QMOE_ACT["swiglu"] else N
         if output is None:
-            output = torch.empty((M, No), dtype=input.dtype, device=input.device)
-        preact = torch.empty((M, N), dtype=input.dtype, device=input.device) if keep_preact else None
-        need = qmoe_linear_workspace_size(input, weights, bias, residual, offsets, a, output, preact)
-        p, n, _keep = _workspace(workspace, need, input.device)
-        _ok(_lib().qmoe_linear(*[_ref(t, True) for t in (input, weights, bias, residual, offsets)], ctypes.byref(a),
-                               _ref(output, True), _ref(preact, True), p, n, st), "qmoe_linear")
+            output = input.new_empty((M, N // 2 if a.activation_type == QMOE_ACT["swiglu"] else N))
+        preact = input.new_empty((M, N)) if keep_preact else None
+        lib, need, attr = _lib(), ctypes.c_size_t(0), ctypes.byref(a)
+        t = _pack((input, weights, bias, residual, offsets, output, preact))
+        _ok(lib.qmoe_linear_workspace_size(*t[:5], attr, t[5], t[6], ctypes.byref(need)), "qmoe_linear_workspace_size")
+        w, n, _keep = _ws(workspace, need.value, input)
+        _ok(lib.qmoe_linear(*t[:5], attr, t[5], t[6], w, n, st), "qmoe_linear")
     return (output, preact) if keep_preact else output
 
 
@@ -732,10 +799,9 @@ def qmoe_linear_backward_workspace_size(grad_output, input, weights, preact=None
     """Workspace bytes of qmoe_linear_backward for the gradients given.  Arrays may live anywhere."""
     a, n = _linear_a(attrs), ctypes.c_size_t(0)
     _ok(_lib().qmoe_linear_backward_workspace_size(
-        *[_ref(t, False) for t in (grad_output, input, weights, preact, offsets)], ctypes.byref(a),
-        *[_ref(t, False) for t in (grad_input, grad_weights, grad_bias)], ctypes.byref(n)),
-        "qmoe_linear_backward_workspace_size")
-    return int(n.value)
+        *_refs(grad_output, input, weights, preact, offsets), ctypes.byref(a),
+        *_refs(grad_input, grad_weights, grad_bias), ctypes.byref(n)), "qmoe_linear_backward_workspace_size")
+    return n.value
 
 
 def qmoe_linear_backward(grad_output, input, weights, preact, offsets, attrs, grad_input, grad_weights, grad_bias,
@@ -743,12 +809,12 @@ def qmoe_linear_backward(grad_output, input, weights, preact, offsets, attrs, gr
     """Enqueue the gradients of qmoe_linear (any may be None); preact None for
     the identity, offsets None for a dense layer."""
     a = _linear_a(attrs)
-    with _on(stream, (grad_output, input, weights, preact, offsets, grad_input, grad_weights, grad_bias,
-                      workspace)) as st:
-        p, n, _keep = _workspace(workspace, 0 if workspace is None else 1, input.device)
-        _ok(_lib().qmoe_linear_backward(
-            *[_ref(t, True) for t in (grad_output, input, weights, preact, offsets)], ctypes.byref(a),
-            *[_ref(t, True) for t in (grad_input, grad_weights, grad_bias)], p, n, st), "qmoe_linear_backward")
+    ctx, st = _on(stream, (grad_output, input, weights, preact, offsets, grad_input, grad_weights, grad_bias,
+                           workspace))
+    with ctx:
+        w, n, _keep = _ws(workspace, 0, input)
+        t = _pack((grad_output, input, weights, preact, offsets, grad_input, grad_weights, grad_bias))
+        _ok(_lib().qmoe_linear_backward(*t[:5], ctypes.byref(a), *t[5:], w, n, st), "qmoe_linear_backward")
 
 
 def linear_backward(grad_output, input, weights, preact=None, offsets=None, attrs=None, bias=False, stream=None,
@@ -757,12 +823,14 @@ def linear_backward(grad_output, input, weights, preact=None, offsets=None, attr
     grad_bias None unless ``bias``."""
     import torch
     a = _linear_a(attrs)
-    with _on(stream, (grad_output, input, weights, preact, offsets, workspace)) as st:
+    ctx, st = _on(stream, (grad_output, input, weights, preact, offsets, workspace))
+    with ctx:
         gi, gw = torch.empty_like(input), torch.empty_like(weights)
-        gb = torch.empty(weights.shape[:-1], dtype=weights.dtype, device=weights.device) if bias else None
-        need = qmoe_linear_backward_workspace_size(grad_output, input, weights, preact, offsets, a, gi, gw, gb)
-        p, n, _keep = _workspace(workspace, need, input.device)
-        _ok(_lib().qmoe_linear_backward(
-            *[_ref(t, True) for t in (grad_output, input, weights, preact, offsets)], ctypes.byref(a),
-            *[_ref(t, True) for t in (gi, gw, gb)], p, n, st), "qmoe_linear_backward")
+        gb = weights.new_empty(weights.shape[:-1]) if bias else None
+        lib, need, attr = _lib(), ctypes.c_size_t(0), ctypes.byref(a)
+        t = _pack((grad_output, input, weights, preact, offsets, gi, gw, gb))
+        _ok(lib.qmoe_linear_backward_workspace_size(*t[:5], attr, *t[5:], ctypes.byref(need)),
+            "qmoe_linear_backward_workspace_size")
+        w, n, _keep = _ws(workspace, need.value, input)
+        _ok(lib.qmoe_linear_backward(*t[:5], attr, *t[5:], w, n, st), "qmoe_linear_backward")
     return gi, gw, gb

@@ -258,6 +258,28 @@ __global__ void __launch_bounds__(64 * WQ * WP) qmoe_linear(const LinearGemm g, 
 #pragma unroll
     for (int b = 0; b < TQ; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
   const int wq = wave / WP, wp = wave % WP;
+  // float32: the sums of every kFold stages (256 r) are added up on their own,
+  // so that a long sum's error grows with its square root over 256 twice
+  // instead of once over all (8192 terms: 1.2e-6 -> 4e-7 of the result)
+  constexpr int kFold = sizeof(ET) == 4 ? 8 : 0;
+  f32x4 sum[kFold ? TP : 1][kFold ? TQ : 1];
+  if constexpr (kFold > 0) {
+#pragma unroll
+    for (int a = 0; a < TP; ++a)
+#pragma unroll
+      for (int b = 0; b < TQ; ++b) sum[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  auto fold = [&]() QMOE_INLINE {
+    if constexpr (kFold > 0) {
+#pragma unroll
+      for (int a = 0; a < TP; ++a)
+#pragma unroll
+        for (int b = 0; b < TQ; ++b) {
+          sum[a][b] += acc[a][b];
+          acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+    }
+  };
 
   // Load instruction i of stage kt into place u (= kt % NST); past the range's
   // end zeros, so that the count of loads in flight stays the same.
@@ -292,13 +314,12 @@ __global__ void __launch_bounds__(64 * WQ * WP) qmoe_linear(const LinearGemm g, 
   // block (the TP products of one q fragment).  The next step's operands are
   // read meanwhile: a q fragment into its own registers when its block is
   // done, the p fragments into a second set.  In the stage's second step all
-  // of the stage has been read, so after the first blocks (which cover the
-  // last reads) the workgroup meets; behind the barrier the reads go to the
+  // of the stage has been read, so behind the first block (which covers the
+  // last reads; one block later cost 3 %) the workgroup meets; behind the barrier the reads go to the
   // next stage and this stage's place is filled anew, NST stages ahead, a few
   // loads a block.  The scheduling barriers keep that order.
-  constexpr int kMeet = 0;  // the block behind which the workgroup meets
-  constexpr int kFill = (kStage + TQ - kMeet - 1) / (TQ - kMeet);  // loads a block behind it
-  constexpr int kPer = (TP + TQ - kMeet - 1) / (TQ - kMeet);       // p reads a block
+  constexpr int kFill = (kStage + TQ - 1) / TQ;  // loads a block
+  constexpr int kPer = (TP + TQ - 1) / TQ;       // p reads a block
   auto block = [&](int b, int ks) QMOE_INLINE {
 #pragma unroll
     for (int a = 0; a < TP; ++a) acc[a][b] = LinMma<ET>::mma(fp[ks][a], fq[b], acc[a][b]);
@@ -331,22 +352,27 @@ __global__ void __launch_bounds__(64 * WQ * WP) qmoe_linear(const LinearGemm g, 
         for (int b = 0; b < TQ; ++b) {
           block(b, 1);
           __builtin_amdgcn_sched_barrier(0);
-          if (b == kMeet) meet();
-          if (b < kMeet) continue;
+          if (b == 0) meet();
           const int n = (u + 1) % NST;
-          if (b == kMeet)
-#pragma unroll
-            for (int c = 0; c < kMeet; ++c) read_q(c, n, 0);
           read_q(b, n, 0);
 #pragma unroll
-          for (int a = (b - kMeet) * kPer; a < (b - kMeet + 1) * kPer && a < TP; ++a) read_p(a, n, 0);
+          for (int a = b * kPer; a < (b + 1) * kPer && a < TP; ++a) read_p(a, n, 0);
 #pragma unroll
-          for (int i = (b - kMeet) * kFill; i < (b - kMeet + 1) * kFill && i < kStage; ++i) load(i, kt + u + NST, u);
+          for (int i = b * kFill; i < (b + 1) * kFill && i < kStage; ++i) load(i, kt + u + NST, u);
+        }
+        if constexpr (kFold > 0) {
+          if ((kt + u) % kFold == kFold - 1) fold();
         }
       }
     }
   }
   lin_wait<0>();  // no load outlives the workgroup
+  if constexpr (kFold > 0) {
+#pragma unroll
+    for (int a = 0; a < TP; ++a)
+#pragma unroll
+      for (int b = 0; b < TQ; ++b) acc[a][b] += sum[a][b];
+  }
 
   // acc[a][b][i]: column 4 (lane / 16) + i, row lane % 16 of its 16 x 16
   // block.  The sums go through LDS, 32 rows of every wavefront at a time, so

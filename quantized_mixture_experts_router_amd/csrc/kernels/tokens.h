@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 namespace qmoe {
 
 enum RowType { ROW_F32 = 0, ROW_F16 = 1, ROW_BF16 = 2 };
@@ -16,18 +18,21 @@ hipError_t launch_route_topk(const float* logits, int T, int E, int k, bool over
 hipError_t launch_route_grad(const float* gw, const float* logits, const void* idx, bool idx64, int T, int E, int k,
                              bool over_all, float* gl, hipStream_t st);
 
-// Slots per block of the expert sort, and its block count, for S slots.
+// Slots per block of the expert sort.  Up to kSortSelf slots every block
+// counts the experts of all slots itself (12288 slots: one launch of 24
+// blocks, against a counting launch and one block per 1024); beyond, a first
+// launch counts per block, with at most 256 blocks (each adds up the others').
 constexpr int kSortRound = 512;
+constexpr int kSortSelf = 16384;
 inline int sort_chunk(long S) {
-  const long c = (S + 255) / 256;  // at most 256 blocks (each adds up the others' counts)
-  const long least = S <= 4096 ? 4096 : 1024;
-  const long v = c > least ? c : least;
-  return (int)((v + kSortRound - 1) / kSortRound * kSortRound);
+  if (S <= kSortSelf) return kSortRound;
+  const long c = std::max((S + 255) / 256, 1024l);
+  return (int)((c + kSortRound - 1) / kSortRound * kSortRound);
 }
 // Stable sort of the S slots by expert: offsets [E + 1], perm [S] (may be
 // NULL), inverse [S] (place, or -1 - place of a slot whose index lies outside
-// [0, E): those follow the last expert, in slot order).  hist: nchunks x
-// (E + 1) ints when there is more than one block.
+// [0, E): those follow the last expert, in slot order).  hist: blocks x
+// (E + 1) ints beyond kSortSelf slots.
 hipError_t launch_sort_slots(const void* idx, bool idx64, int S, int E, int* hist, int* offsets, int* perm,
                              int* inverse, hipStream_t st);
 

@@ -201,9 +201,10 @@ __global__ void __launch_bounds__(kSortRound) qmoe_sort_count(const void* __rest
 }
 
 // Places of a chunk's slots.  The block adds up the chunks' counts itself
-// (first place of every expert in this chunk), then ranks 512 slots a round:
-// lanes of one wavefront with the same expert find each other with a ballot
-// per bit of the expert's number, wavefronts in order through LDS counts.
+// (first place of every expert in this chunk; hist NULL: it counts them from
+// the indices), then ranks 512 slots a round: lanes of one wavefront with the
+// same expert find each other with a ballot per bit of the expert's number,
+// wavefronts in order through LDS counts.
 __global__ void __launch_bounds__(kSortRound) qmoe_sort_place(const void* __restrict__ idx, bool idx64, int S, int E,
                                                               int chunk, int nchunks, const int* __restrict__ hist,
                                                               int* __restrict__ offsets, int* __restrict__ perm,
@@ -215,10 +216,17 @@ __global__ void __launch_bounds__(kSortRound) qmoe_sort_place(const void* __rest
   int* wcnt = sm + B;      // [NW][B] counts of a round's wavefronts
   __shared__ int wsum[NW];
   const int lane = lane_id(), wave = threadIdx.x >> 6;
-  if (nchunks == 1) {
-    for (int e = threadIdx.x; e < B; e += kSortRound) base[e] = 0;
+  const int s0 = blockIdx.x * chunk, s1 = min(S, s0 + chunk);
+  if (!hist) {
+    for (int e = threadIdx.x; e < 2 * B; e += kSortRound) sm[e] = 0;
     __syncthreads();
-    for (int s = threadIdx.x; s < S; s += kSortRound) atomicAdd(&base[bucket(idx, idx64, s, E)], 1);
+    // (the whole array in base, what comes before the chunk in wcnt)
+#pragma unroll 4
+    for (int s = threadIdx.x; s < S; s += kSortRound) {
+      const int e = bucket(idx, idx64, s, E);
+      atomicAdd(&base[e], 1);
+      if (s < s0) atomicAdd(&wcnt[e], 1);
+    }
     __syncthreads();
   }
   // totals of buckets 2 i and 2 i + 1 in thread i (B <= 1024), and this
@@ -228,8 +236,9 @@ __global__ void __launch_bounds__(kSortRound) qmoe_sort_place(const void* __rest
   for (int h = 0; h < 2; ++h) {
     const int e = 2 * threadIdx.x + h;
     if (e >= B) continue;
-    if (nchunks == 1) {
+    if (!hist) {
       tot[h] = base[e];
+      before[h] = wcnt[e];
     } else {
 #pragma unroll 8
       for (int c = 0; c < nchunks; ++c) {
@@ -260,7 +269,6 @@ __global__ void __launch_bounds__(kSortRound) qmoe_sort_place(const void* __rest
   }
   int bits = 0;
   while ((1 << bits) < B) ++bits;
-  const int s0 = blockIdx.x * chunk, s1 = min(S, s0 + chunk);
   for (int r0 = s0; r0 < s1; r0 += kSortRound) {
     for (int i = threadIdx.x; i < NW * B; i += kSortRound) wcnt[i] = 0;
     __syncthreads();
@@ -501,7 +509,8 @@ hipError_t launch_sort_slots(const void* idx, bool idx64, int S, int E, int* his
                              int* inverse, hipStream_t st) {
   const int chunk = sort_chunk(S), n = S > 0 ? (S + chunk - 1) / chunk : 1;
   const size_t B = E + 1;
-  if (n > 1)
+  if (S <= kSortSelf) hist = nullptr;
+  else
     hipLaunchKernelGGL(qmoe_sort_count, dim3(n), dim3(kSortRound), B * sizeof(int), st, idx, idx64, S, E, chunk, hist);
   hipLaunchKernelGGL(qmoe_sort_place, dim3(n), dim3(kSortRound), (1 + kSortRound / 64) * B * sizeof(int), st, idx,
                      idx64, S, E, chunk, n, hist, offsets, perm, inverse);

@@ -40,27 +40,42 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Tile shape and ranges of the reduction for a product of `rows` output rows
 // (of `groups` groups, the rows spread over them evenly as far as the host
-// can know) by `cols` columns summed over `red`.
+// can know) by `cols` columns summed over `red`: the least of an estimate in
+// microseconds.  A compute unit runs ceil(items / 256) items one after the
+// other; an item costs its stages (128 bytes of r a row) and a fixed part
+// (first loads, output).  Both were measured on full cards: 4096 x 4096
+// outputs, K = 4096, at 1.25 PFLOP/s (256 x 256), 0.91 (128 x 128), 0.81
+// (64 x 128) and 0.58 (32 x 128) in bfloat16, 139, 141 and 135 TFLOP/s in
+// float32.  Ranges add the float32 sums' way to memory and back and one more
+// launch.
 LinearPlan plan_product(int type, int64_t rows, int64_t groups, int64_t cols, int64_t red) {
   static const struct {
     int tile;
     int64_t bq, bp;
-    double rate;  // of the matrix cores a full card reaches with this tile, relative
-  } tiles[] = {{LT_256x256, 256, 256, 1.0}, {LT_128x128, 128, 128, 0.7}, {LT_64x128, 64, 128, 0.5}, {LT_32x128, 32, 128, 0.3}};
+    double stage16, stage32, fixed;
+  } tiles[] = {{LT_256x256, 256, 256, 1.60, 0.0, 6.0},
+               {LT_128x128, 128, 128, 0.60, 1.93, 2.5},
+               {LT_64x128, 64, 128, 0.33, 0.95, 1.4},
+               {LT_32x128, 32, 128, 0.23, 0.50, 0.9}};
   const int64_t cus = 256, bk = type == LIN_F32 ? 32 : 64;
-  const int64_t per = std::max<int64_t>(1, ceil_div(rows, groups));
+  const int64_t per = std::max<int64_t>(1, ceil_div(rows, groups)), stages = std::max<int64_t>(1, ceil_div(red, bk));
   LinearPlan best{LT_32x128, 1};
   double best_cost = -1;
   for (const auto& t : tiles) {
-    if (type == LIN_F32 && t.tile == LT_256x256) continue;
+    const double stage = type == LIN_F32 ? t.stage32 : t.stage16;
+    if (stage == 0.0) continue;
     const int64_t n = ceil_div(per, t.bq) * std::min(groups, rows) * ceil_div(cols, t.bp);
-    const double cost = (double)ceil_div(n, cus) * t.bq * t.bp / t.rate;
-    if (best_cost < 0 || cost < best_cost) {
-      best_cost = cost;
-      best.tile = t.tile;
-      // ranges of the reduction when the tiles leave compute units idle, at
-      // least eight steps each
-      best.splits = (int)std::max<int64_t>(1, std::min<int64_t>({cus / std::max<int64_t>(1, n), red / (8 * bk), 32}));
+    for (int64_t s : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
+      if (s > 1 && stages < 4 * s) break;  // at least four stages a range
+      // (alone on its compute unit a float32 item leaves the matrix cores a fifth idle)
+      const double slow = type == LIN_F32 && n * s <= cus ? 1.2 : 1.0;
+      double cost = (double)ceil_div(n * s, cus) * (t.fixed + (double)ceil_div(stages, s) * stage * slow);
+      if (s > 1) cost += 4.0 + (double)s * (double)rows * (double)cols * 8.0 / 4.5e6;
+      if (best_cost < 0 || cost < best_cost) {
+        best_cost = cost;
+        best.tile = t.tile;
+        best.splits = (int)s;
+      }
     }
   }
   return best;

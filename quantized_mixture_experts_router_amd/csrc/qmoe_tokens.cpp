@@ -168,7 +168,7 @@ qmoe_status check_dispatch(const qmoe_tensor* input, const qmoe_tensor* indices,
   if (perm && !is(perm, {T * k})) return QMOE_ERR_SHAPE;
   if (inverse && !is(inverse, {T, k})) return QMOE_ERR_SHAPE;
   const int64_t S = T * k, chunk = sort_chunk(S), n = (S + chunk - 1) / chunk;
-  *bytes = n > 1 ? (size_t)(n * (experts + 1)) * sizeof(int32_t) : 0;
+  *bytes = S > kSortSelf ? (size_t)(n * (experts + 1)) * sizeof(int32_t) : 0;
   return QMOE_OK;
 }
 

@@ -164,7 +164,7 @@ def _check_rows(torch, dt, T, H, E, k, kind, idx_type="int32", seed=0):
 @pytest.mark.parametrize("T,H,E,k,kind", [
     (1, 1, 1, 1, "any"), (1, 4096, 8, 2, "any"), (16, 64, 8, 2, "wild"), (3, 17, 5, 3, "wild"), (70, 136, 64, 6, "any"),
     (513, 24, 130, 8, "wild"), (100, 33, 1023, 10, "any"), (9, 2056, 4, 4, "one"), (6, 40, 3, 2, "none"),
-    (1100, 9, 7, 4, "one")])
+    (1100, 9, 7, 4, "one"), (2048, 16, 64, 8, "wild"), (2049, 16, 64, 8, "any")])
 def test_rows(torch, dt, T, H, E, k, kind):
     _check_rows(torch, dt, T, H, E, k, kind, "int64" if T % 2 == 0 and kind != "wild" else "int32", seed=T)
 

@@ -78,11 +78,11 @@ def _dispatch(lib, x=T(BF16, 6, 10), idx=T(I32, 6, 2), experts=4, rows=T(BF16, 1
     (dict(off=T(I64, 5)), DTYPE), (dict(perm=T(I32, 11)), SHAPE), (dict(inv=T(I32, 12)), SHAPE),
     (dict(experts=-1), ATTR), (dict(experts=1024), UNSUPPORTED), (dict(x=T(BF16, 6, 10, ptr=None)), NULL),
     (dict(rows=T(BF16, 12, 10, ptr=GOOD + 1)), ALIGN), (dict(x=T(BF16, 6, -1)), SHAPE),
-    # 8192 slots need a workspace
-    (dict(x=T(BF16, 4096, 10), idx=T(I32, 4096, 2), rows=T(BF16, 8192, 10), perm=None, inv=T(I32, 4096, 2)), NULL),
-    (dict(x=T(BF16, 4096, 10), idx=T(I32, 4096, 2), rows=T(BF16, 8192, 10), perm=None, inv=T(I32, 4096, 2), ws=GOOD,
+    # 32768 slots need a workspace
+    (dict(x=T(BF16, 16384, 10), idx=T(I32, 16384, 2), rows=T(BF16, 32768, 10), perm=None, inv=T(I32, 16384, 2)), NULL),
+    (dict(x=T(BF16, 16384, 10), idx=T(I32, 16384, 2), rows=T(BF16, 32768, 10), perm=None, inv=T(I32, 16384, 2), ws=GOOD,
           n=8), WORKSPACE),
-    (dict(x=T(BF16, 4096, 10), idx=T(I32, 4096, 2), rows=T(BF16, 8192, 10), perm=None, inv=T(I32, 4096, 2),
+    (dict(x=T(BF16, 16384, 10), idx=T(I32, 16384, 2), rows=T(BF16, 32768, 10), perm=None, inv=T(I32, 16384, 2),
           ws=GOOD + 64, n=1 << 20), ALIGN)])
 def test_dispatch_refusals(lib, kw, want):
     assert _dispatch(lib, **kw) == want
@@ -91,8 +91,8 @@ def test_dispatch_refusals(lib, kw, want):
 def test_dispatch_workspace(lib):
     n = ctypes.c_size_t(7)
     size = lambda t, k, e: lib.qmoe_dispatch_workspace_size(R(T(F32, t, 8)), R(T(I64, t, k)), e, ctypes.byref(n))  # noqa: E731
-    assert size(2048, 2, 64) == 0 and n.value == 0
-    assert size(2049, 2, 64) == 0 and n.value > 0
+    assert size(8192, 2, 64) == 0 and n.value == 0
+    assert size(8193, 2, 64) == 0 and n.value > 0
     assert size(1 << 22, 8, 1023) == 0 and n.value <= 256 * 1024 * 4  # at most 256 blocks' counts
     assert size(1 << 27, 8, 64) == UNSUPPORTED
     assert lib.qmoe_dispatch_workspace_size(R(T(F32, 4, 8)), R(T(I64, 4, 1)), 4, None) == NULL
