@@ -39,13 +39,13 @@ __device__ __forceinline__ float lin_swiglu(float g, float u, const LinearAct& a
 }
 
 // d act / dz times dy
-__device__ __forceinline__ float lin_act_grad(float dy, float z, const LinearAct& a) {
-  if (a.type == kActRelu) return z > 0.f ? dy : 0.f;
-  if (a.type == kActGelu) {
+__device__ __forceinline__ float lin_act_grad(float dy, float z, int act) {
+  if (act == kActRelu) return z > 0.f ? dy : 0.f;
+  if (act == kActGelu) {
     const float cdf = 0.5f * (1.f + erff(z * 0.70710678118654752f));
     return dy * (cdf + z * 0.39894228040143268f * expf(-0.5f * z * z));
   }
-  if (a.type == kActSilu) {
+  if (act == kActSilu) {
     const float s = lin_sigmoid(z);
     return dy * s * (1.f + z * (1.f - s));
   }
@@ -80,45 +80,70 @@ __device__ __forceinline__ void group_rows(const int* __restrict__ offsets, int 
   hi = g < G ? min(max(offsets[g + 1], lo), M) : M;
 }
 
-// Row block b (bm rows of one group each, the groups in order, then the rows
-// behind the last group as group G): its group and rows [lo, hi) from the
-// block's first row on (hi = the group's end).  False: past the last block.
-// Every lane of a wavefront gets the same answer.
-__device__ __forceinline__ bool find_block(const int* __restrict__ offsets, int G, int M, int bm, int b, int& g,
-                                           int& lo, int& hi) {
-  if (!offsets) {
-    g = 0;
-    lo = b * bm;
-    hi = M;
-    return lo < M;
-  }
-  const int lane = lane_id();
-  int seen = 0;
-  for (int c = 0; c <= G; c += 64) {
-    int l = 0, h = 0;
-    if (c + lane <= G) group_rows(offsets, G, M, c + lane, l, h);
-    const int n = (h - l + bm - 1) / bm;
-    int inc = n;
+// The rows of up to G + 1 groups (group G: the rows behind the last) as blocks
+// of bm rows of one group each, in group order.  Every lane of a wavefront gets
+// the same answers; groups 0 .. 63 stay in registers, a lane each.
+struct RowBlocks {
+  const int* offsets;
+  int G, M, bm;
+  int lo, n, inc;  // lane's group of the first 64: first row, blocks, blocks up to its end
+  int hi;
+  int total;       // blocks in all
+
+  __device__ __forceinline__ void scan(int g, int& l, int& h, int& c, int& i) const {
+    l = h = 0;
+    if (g <= G) group_rows(offsets, G, M, g, l, h);
+    c = (h - l + bm - 1) / bm;
+    i = c;
+    const int lane = lane_id();
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
-      const int v = __shfl_up(inc, o);
-      if (lane >= o) inc += v;
+      const int v = __shfl_up(i, o);
+      if (lane >= o) i += v;
     }
-    const unsigned long long past = __ballot(seen + inc > b);
-    if (past) {
-      const int f = __ffsll((long long)past) - 1;
-      const int first = __shfl(seen + inc - n, f);
-      g = __builtin_amdgcn_readfirstlane(c + f);
-      lo = __builtin_amdgcn_readfirstlane(__shfl(l, f) + (b - first) * bm);
-      hi = __builtin_amdgcn_readfirstlane(__shfl(h, f));
+  }
+  __device__ __forceinline__ RowBlocks(const int* __restrict__ offs, int g, int m, int b)
+      : offsets(offs), G(g), M(m), bm(b) {
+    if (!offsets) {
+      total = (M + bm - 1) / bm;
+      return;
+    }
+    scan(lane_id(), lo, hi, n, inc);
+    total = __builtin_amdgcn_readlane(inc, 63);
+    for (int c = 64; c <= G; c += 64) {
+      int l, h, k, i;
+      scan(c + lane_id(), l, h, k, i);
+      total += __builtin_amdgcn_readlane(i, 63);
+    }
+  }
+  // Block b: its group and rows [l, h) from the block's first row on (h = the
+  // group's end).  False: past the last block.
+  __device__ __forceinline__ bool find(int b, int& g, int& l, int& h) const {
+    if (b >= total) return false;
+    if (!offsets) {
+      g = 0;
+      l = b * bm;
+      h = M;
       return true;
     }
-    seen += __shfl(inc, 63);
+    int seen = 0, cl = lo, ch = hi, cn = n, ci = inc;
+    for (int c = 0;; c += 64) {
+      const unsigned long long past = __ballot(seen + ci > b);
+      if (past) {
+        const int f = __ffsll((long long)past) - 1;
+        g = c + f;
+        l = __builtin_amdgcn_readlane(cl, f) + (b - seen - __builtin_amdgcn_readlane(ci - cn, f)) * bm;
+        h = __builtin_amdgcn_readlane(ch, f);
+        return true;
+      }
+      if (c + 64 > G) return false;
+      seen += __builtin_amdgcn_readlane(ci, 63);
+      scan(c + 64 + lane_id(), cl, ch, cn, ci);
+    }
   }
-  return false;
-}
+};
 
-// First row block of group g (find_block's order) and its count of blocks.
+// First row block of group g (RowBlocks' order) and its count of blocks.
 __device__ __forceinline__ void group_blocks(const int* __restrict__ offsets, int G, int M, int bm, int g, int& first,
                                              int& count) {
   first = 0;
@@ -249,7 +274,7 @@ __device__ __forceinline__ void linear_rows(const LinearGemm& g, float (&z)[R][W
 
 // f(ACT) with the activation as a compile-time constant.
 template <typename F>
-__device__ __forceinline__ void with_act(int act, F f) {
+__host__ __device__ __forceinline__ void with_act(int act, F f) {
   switch (act) {
     case kActRelu: f(std::integral_constant<int, kActRelu>{}); break;
     case kActSwiglu: f(std::integral_constant<int, kActSwiglu>{}); break;

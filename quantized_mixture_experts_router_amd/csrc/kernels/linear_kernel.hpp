@@ -184,19 +184,20 @@ struct LinOperand {
 };
 
 // Output tiles are taken in runs of up to 32 per XCD (workgroups go to the 8
-// XCDs in turn; 32 compute units each; shorter runs when there are fewer tiles
-// than compute units), inside a run eight q blocks by four p blocks, so that a
-// run's operand rows are shared in its XCD's L2.
-__device__ __forceinline__ void tile_of(int b, int run, int nq, int np, int& q, int& p) {
-  const int t = ((b >> 3) / run * 8 + (b & 7)) * run + (b >> 3) % run;
+// XCDs in turn; 32 compute units each; every XCD gets the same number of runs),
+// inside a run eight q blocks by four p blocks, so that a run's operand rows
+// are shared in its XCD's L2.
+__device__ __forceinline__ void tile_of(int b, int nq, int np, int& q, int& p) {
   const int h = min(nq, 8);
+  const int share = ((nq + h - 1) / h * h * np + 7) >> 3, runs = (share + 31) >> 5, run = (share + runs - 1) / runs;
+  const int t = ((b >> 3) / run * 8 + (b & 7)) * run + (b >> 3) % run;
   const int s = t / (h * np), r = t - s * (h * np);
   q = s * h + r % h;
   p = r / h;
 }
 
 template <typename ET, int MODE, int BQ, int BP, int WQ, int WP, int NST, bool VEC>
-__global__ void __launch_bounds__(64 * WQ * WP) qmoe_linear(const LinearGemm g, int run, int nq, int np) {
+__global__ void __launch_bounds__(64 * WQ * WP) qmoe_linear(const LinearGemm g, int nq, int np) {
   constexpr int NW = WQ * WP, TQ = BQ / WQ / 16, TP = BP / WP / 16;
   using OP = LinOperand<ET, BP, MODE == LIN_FWD, NW>;
   using OQ = LinOperand<ET, BQ, MODE != LIN_DW, NW>;
@@ -206,7 +207,11 @@ __global__ void __launch_bounds__(64 * WQ * WP) qmoe_linear(const LinearGemm g, 
 
   int qb, pb;
   const int ks_id = blockIdx.y;  // range of r
-  tile_of(blockIdx.x, run, nq, np, qb, pb);
+  // (in rows of groups only the device knows how many blocks there are)
+  const RowBlocks blocks(MODE == LIN_DW ? nullptr : g.offsets, g.G, g.M, BQ);
+  if (MODE != LIN_DW && g.offsets) nq = blocks.total;
+  if (nq <= 0) return;
+  tile_of(blockIdx.x, nq, np, qb, pb);
   const int p0 = pb * BP;
   int grp, lo, hi, q0, qrows;  // group, its rows from the tile on, first output row, valid rows of the tile
   const int pcols = MODE == LIN_FWD ? g.N : g.K;
@@ -223,7 +228,7 @@ __global__ void __launch_bounds__(64 * WQ * WP) qmoe_linear(const LinearGemm g, 
     group_rows(g.offsets, g.G, g.M, grp, lo, hi);
     R = hi - lo;
   } else {
-    if (!find_block(g.offsets, g.G, g.M, BQ, qb, grp, lo, hi)) return;
+    if (!blocks.find(qb, grp, lo, hi)) return;
     q0 = lo;
     qrows = hi - lo;
     if (grp == g.G && g.offsets) {  // rows behind the last group: zeros
@@ -460,12 +465,13 @@ hipError_t go_linear(const LinearGemm& g, bool vec, hipStream_t st) {
   const long qb = (rows + BQ - 1) / BQ;
   const long nq = MODE == LIN_DW ? qb * g.G : g.offsets ? qb + g.G + 1 : qb;
   const long np = (cols + BP - 1) / BP;
+  // workgroups for the most tiles there can be (tile_of's runs cover at most
+  // these)
   const long h = nq < 8 ? nq : 8;
-  const long n = (nq + h - 1) / h * h * np;  // whole runs of h q blocks
-  const long run = n >= 256 ? 32 : (n + 7) / 8;
-  const dim3 grid((unsigned)((n + 8 * run - 1) / (8 * run) * (8 * run)), (unsigned)g.splits), block(64 * WQ * WP);
-  if (vec) hipLaunchKernelGGL((qmoe_linear<ET, MODE, BQ, BP, WQ, WP, NST, true>), grid, block, 0, st, g, (int)run, (int)nq, (int)np);
-  else hipLaunchKernelGGL((qmoe_linear<ET, MODE, BQ, BP, WQ, WP, NST, false>), grid, block, 0, st, g, (int)run, (int)nq, (int)np);
+  const long share = ((nq + h - 1) / h * h * np + 7) / 8;
+  const dim3 grid((unsigned)((share <= 32 ? share : (share + 31) / 32 * 32) * 8), (unsigned)g.splits), block(64 * WQ * WP);
+  if (vec) hipLaunchKernelGGL((qmoe_linear<ET, MODE, BQ, BP, WQ, WP, NST, true>), grid, block, 0, st, g, (int)nq, (int)np);
+  else hipLaunchKernelGGL((qmoe_linear<ET, MODE, BQ, BP, WQ, WP, NST, false>), grid, block, 0, st, g, (int)nq, (int)np);
   return hipGetLastError();
 }
 

@@ -1,6 +1,8 @@
 // The linear layers' passes beside the matrix kernel (linear.h): the sum of
 // split reductions with the epilogue, the activation's gradient with column
 // sums, the bias gradient and row padding.  All are bound by HBM.
+#include <algorithm>
+
 #include "linear_common.hpp"
 
 namespace qmoe {
@@ -8,7 +10,7 @@ namespace qmoe {
 namespace {
 
 // Group of output row m (rows behind the last group: G): binary search for
-// the first group whose end lies past m; offsets as find_block takes them.
+// the first group whose end lies past m; offsets as group_rows takes them.
 __device__ __forceinline__ int group_of_row(const int* __restrict__ offsets, int G, int M, int m) {
   if (!offsets) return 0;
   int a = 0, b = G;
@@ -72,98 +74,93 @@ hipError_t finish_mode(int mode, const LinearGemm& g, hipStream_t st) {
   return go_finish<ET, LIN_DW>(g, st);
 }
 
-// dz of kSumRows rows of one group by 4 * 64 columns a wavefront, four
-// columns a lane, and their column sums (float32, of the unrounded dz, in row
-// order: the four wavefronts take every fourth row each and add up in
-// wavefront order through LDS).
-template <typename ET, bool VEC>
+// dz of kSumRows rows of one group, W columns a lane (16 bytes where rows
+// allow it, VEC), and their column sums: float32, of the unrounded dz, in row
+// order (the four wavefronts take every fourth row each and add up in
+// wavefront order through LDS).  Four rows of a wavefront are in flight at a
+// time.
+template <typename ET, int ACT, bool VEC>
 __global__ void __launch_bounds__(256) qmoe_linear_act_grad(const LinearActGrad g, int ncol) {
-  using V4 = typename LinVec4<ET>::type;
-  using V2 = typename LinVec2<ET>::type;
-  __shared__ f32x4 red[3][64];
+  constexpr int W = VEC ? 16 / (int)sizeof(ET) : 4, R = 4;
+  constexpr bool glu = ACT == kActSwiglu;
+  constexpr int H = glu ? W / 2 : W;
+  __shared__ float red[3][64][W + 1];
   const int rb = blockIdx.x / ncol;
   int grp, lo, hi;
-  if (!find_block(g.offsets, g.G, g.M, kSumRows, rb, grp, lo, hi) || grp >= g.G) return;  // the whole workgroup
+  if (!RowBlocks(g.offsets, g.G, g.M, kSumRows).find(rb, grp, lo, hi) || grp >= g.G) return;  // the whole workgroup
   const int lane = lane_id(), wave = threadIdx.x >> 6;
-  const int n = (blockIdx.x % ncol) * 256 + 4 * lane;
-  const bool glu = g.act.type == kActSwiglu;
+  const int n = ((blockIdx.x % ncol) * 64 + lane) * W;
+  const int left = g.N - n;  // columns from n on
   const long No = glu ? g.N >> 1 : g.N;
   const int m1 = min(hi, lo + kSumRows);
-  const ET* dyp = static_cast<const ET*>(g.dy);
-  const ET* zp = static_cast<const ET*>(g.z);
-  f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-  for (int m = lo + wave; m < m1; m += 4) {
-    f32x4 dz = {0.f, 0.f, 0.f, 0.f};
-    if (VEC ? n < g.N : true) {
-      float z[4] = {0.f, 0.f, 0.f, 0.f}, dy[4] = {0.f, 0.f, 0.f, 0.f};
-      if constexpr (VEC) {
-        if (zp) {
-          const V4 t = *(const V4*)(zp + (long)m * g.N + n);
+  const ET* dyp = static_cast<const ET*>(g.dy) + (glu ? n >> 1 : n);
+  const ET* zp = static_cast<const ET*>(g.z) + n;
+  float sum[W] = {};
+  for (int m = lo + wave; m < m1; m += 4 * R) {
+    float z[R][W], dy[R][H];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) z[i] = (float)t[i];
-        }
-        if (glu) {
-          const V2 t = *(const V2*)(dyp + (long)m * No + (n >> 1));
-          dy[0] = dy[1] = (float)t[0];
-          dy[2] = dy[3] = (float)t[1];
-        } else {
-          const V4 t = *(const V4*)(dyp + (long)m * No + n);
+    for (int r = 0; r < R; ++r) {
+      const long row = m + 4 * r;
+      const bool ok = row < m1 && left > 0;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) dy[i] = (float)t[i];
-        }
-      } else {
+      for (int i = 0; i < H; ++i) dy[r][i] = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (n + i < g.N) {
-            if (zp) z[i] = (float)zp[(long)m * g.N + n + i];
-            dy[i] = (float)dyp[(long)m * No + (glu ? (n + i) >> 1 : n + i)];
-          }
-      }
-      if (glu) {
-#pragma unroll
-        for (int i = 0; i < 4; i += 2) {
-          float a, b;
-          lin_swiglu_grad(dy[i], z[i], z[i + 1], g.act, a, b);
-          dz[i] = a;
-          dz[i + 1] = b;
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) dz[i] = lin_act_grad(dy[i], z[i], g.act);
-      }
-      if constexpr (!VEC) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (n + i >= g.N) dz[i] = 0.f;
+      for (int i = 0; i < W; ++i) z[r][i] = 0.f;
+      if (ok) {
+        load_w<ET, H, VEC>(dyp + row * No, glu ? left >> 1 : left, dy[r]);
+        if constexpr (ACT != kActIdentity) load_w<ET, W, VEC>(zp + row * g.N, left, z[r]);
       }
     }
-    if (g.dz) store_cols4<ET, VEC>(static_cast<ET*>(g.dz) + (long)m * g.lddz, n, (int)g.lddz, dz);
-    sum += dz;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const long row = m + 4 * r;
+      if (row >= m1) continue;
+      float dz[W];
+      if constexpr (glu) {
+#pragma unroll
+        for (int i = 0; i < H; ++i) lin_swiglu_grad(dy[r][i], z[r][2 * i], z[r][2 * i + 1], g.act, dz[2 * i], dz[2 * i + 1]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < W; ++i) dz[i] = lin_act_grad(dy[r][i], z[r][i], ACT);
+      }
+      // (columns from N on have a zero gradient: zeros in dz)
+      if (g.dz && n < g.lddz) store_w<ET, W, VEC>(static_cast<ET*>(g.dz) + row * g.lddz + n, (int)g.lddz - n, dz);
+#pragma unroll
+      for (int i = 0; i < W; ++i) sum[i] += dz[i];
+    }
   }
   if (!g.sums) return;
-  if (wave > 0) red[wave - 1][lane] = sum;
+  if (wave > 0) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) red[wave - 1][lane][i] = sum[i];
+  }
   __syncthreads();
   if (wave > 0) return;
 #pragma unroll
-  for (int w = 0; w < 3; ++w) sum += red[w][lane];
+  for (int w = 0; w < 3; ++w)
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (n + i < g.N) g.sums[(long)rb * g.N + n + i] = sum[i];
+    for (int i = 0; i < W; ++i) sum[i] += red[w][lane][i];
+#pragma unroll
+  for (int i = 0; i < W; ++i)
+    if (i < left) g.sums[(long)rb * g.N + n + i] = sum[i];
 }
 
 template <typename ET>
 hipError_t go_act_grad(const LinearActGrad& g, hipStream_t st) {
   auto al = [](const void* p, uintptr_t m) { return (reinterpret_cast<uintptr_t>(p) & m) == 0; };
-  const uintptr_t a4 = 4 * sizeof(ET) - 1;
-  const bool vec = g.N % 4 == 0 && al(g.z, a4) && al(g.dz, a4) &&
-                   al(g.dy, g.act.type == kActSwiglu ? 2 * sizeof(ET) - 1 : a4) && (!g.dz || g.lddz % 4 == 0) &&
-                   (!g.dz || g.lddz == g.N);
+  const bool glu = g.act.type == kActSwiglu;
+  constexpr int W = 16 / (int)sizeof(ET);
+  const bool vec = g.N % W == 0 && al(g.z, 15) && al(g.dz, 15) && al(g.dy, glu ? 7 : 15);
   const long blocks = linear_sum_blocks(g.M, g.offsets ? g.G : -1);
   const long cols = g.dz && g.lddz > g.N ? g.lddz : g.N;
-  const int ncol = (int)((cols + 255) / 256);
+  const int per = 64 * (vec ? W : 4);
+  const int ncol = (int)((cols + per - 1) / per);
   const dim3 grid((unsigned)(blocks * ncol)), block(256);
-  if (vec) hipLaunchKernelGGL((qmoe_linear_act_grad<ET, true>), grid, block, 0, st, g, ncol);
-  else hipLaunchKernelGGL((qmoe_linear_act_grad<ET, false>), grid, block, 0, st, g, ncol);
+  with_act(g.act.type, [&](auto act) {
+    constexpr int A = decltype(act)::value;
+    if (vec) hipLaunchKernelGGL((qmoe_linear_act_grad<ET, A, true>), grid, block, 0, st, g, ncol);
+    else hipLaunchKernelGGL((qmoe_linear_act_grad<ET, A, false>), grid, block, 0, st, g, ncol);
+  });
   return hipGetLastError();
 }
 
@@ -186,23 +183,30 @@ __global__ void __launch_bounds__(256) qmoe_linear_bias_grad(const float* __rest
 }
 
 // cols elements of each row into rows of ld (whole 16-byte pieces), zeros
-// behind them: one thread a piece, two operands a launch.
+// behind them: a workgroup a row, a thread a piece (the source pieces are
+// aligned to their element only), two operands a launch.
 template <typename U>
-__global__ void __launch_bounds__(256) qmoe_linear_pad(LinearPad a, LinearPad b, long pieces_a, long pieces) {
+__global__ void __launch_bounds__(256) qmoe_linear_pad(LinearPad a, LinearPad b) {
   constexpr int N = 16 / sizeof(U);
   typedef U V __attribute__((ext_vector_type(N)));
-  const long i = (long)blockIdx.x * 256 + threadIdx.x;
-  if (i >= pieces) return;
-  const LinearPad& t = i < pieces_a ? a : b;
-  const long j = i < pieces_a ? i : i - pieces_a;
-  const int per = (int)(t.ld / N);
-  const long r = j / per;
-  const int c = (int)(j - r * per) * N;
-  const U* src = static_cast<const U*>(t.src) + r * t.cols;
-  V v;
+  typedef V VU __attribute__((aligned(sizeof(U))));
+  for (long i = blockIdx.x; i < a.rows + b.rows; i += gridDim.x) {
+    const bool second = i >= a.rows;
+    const long r = second ? i - a.rows : i;
+    const int cols = (int)(second ? b.cols : a.cols), ld = (int)(second ? b.ld : a.ld);
+    const U* src = static_cast<const U*>(second ? b.src : a.src) + r * cols;
+    U* dst = static_cast<U*>(second ? b.dst : a.dst) + r * ld;
+    for (int c = threadIdx.x * N; c < ld; c += 256 * N) {
+      V v;
+      if (c + N <= cols) {
+        v = *(const VU*)(src + c);
+      } else {
 #pragma unroll
-  for (int k = 0; k < N; ++k) v[k] = c + k < t.cols ? src[c + k] : (U)0;
-  *(V*)(static_cast<U*>(t.dst) + r * t.ld + c) = v;
+        for (int k = 0; k < N; ++k) v[k] = c + k < cols ? src[c + k] : (U)0;
+      }
+      *(V*)(dst + c) = v;
+    }
+  }
 }
 
 }  // namespace
@@ -233,12 +237,11 @@ hipError_t launch_linear_bias_grad(int type, const float* sums, const int* offse
 }
 
 hipError_t launch_linear_pad(int esize, const LinearPad& a, const LinearPad& b, hipStream_t st) {
-  const int n = 16 / esize;
-  const long pa = a.rows * (a.ld / n), all = pa + b.rows * (b.ld / n);
-  if (all == 0) return hipSuccess;
-  const dim3 grid((unsigned)((all + 255) / 256)), block(256);
-  if (esize == 4) hipLaunchKernelGGL(qmoe_linear_pad<uint32_t>, grid, block, 0, st, a, b, pa, all);
-  else hipLaunchKernelGGL(qmoe_linear_pad<uint16_t>, grid, block, 0, st, a, b, pa, all);
+  const long rows = a.rows + b.rows;
+  if (rows == 0) return hipSuccess;
+  const dim3 grid((unsigned)std::min<long>(rows, 1 << 20)), block(256);
+  if (esize == 4) hipLaunchKernelGGL(qmoe_linear_pad<uint32_t>, grid, block, 0, st, a, b);
+  else hipLaunchKernelGGL(qmoe_linear_pad<uint16_t>, grid, block, 0, st, a, b);
   return hipGetLastError();
 }
 
