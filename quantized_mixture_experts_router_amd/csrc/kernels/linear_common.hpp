@@ -19,34 +19,46 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 constexpr int kActRelu = 0, kActSwiglu = 1, kActGelu = 2, kActSilu = 3, kActIdentity = 4;
 
 // 1 / (1 + e^-v), finite for every v: e^-v may overflow to infinity, whose
-// reciprocal is the right 0.
-__device__ __forceinline__ float lin_sigmoid(float v) { return 1.f / (1.f + expf(-v)); }
+// reciprocal is the right 0.  FAST (results that are rounded to 16 bits): the
+// hardware's exponential and reciprocal, each within 2^-22 of 1 relative and
+// |v| 2^-24 for the argument's scaling, far below half a step of the types
+// (2^-11, 2^-8); the full ones made the epilogue of a 256 x 256 SwiGLU tile 9 us
+// of arithmetic and bound the activation's gradient pass.
+template <bool FAST>
+__device__ __forceinline__ float lin_sigmoid(float v) {
+  if constexpr (FAST) return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(v * -1.4426950408889634f));
+  return 1.f / (1.f + expf(-v));
+}
 
+template <bool FAST>
 __device__ __forceinline__ float lin_act(float z, int act) {
   if (act == kActRelu) return z < 0.f ? 0.f : z;  // NaN stays NaN
   if (act == kActGelu) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
-  if (act == kActSilu) return z * lin_sigmoid(z);
+  if (act == kActSilu) return z * lin_sigmoid<FAST>(z);
   return z;
 }
 
 // g sigma(alpha g) (u + beta), with a limit L: g <- min(g, L), u <- clamp(u, -L, L)
+template <bool FAST>
 __device__ __forceinline__ float lin_swiglu(float g, float u, const LinearAct& a) {
   if (a.has_limit) {
     g = g > a.limit ? a.limit : g;
     u = u > a.limit ? a.limit : u < -a.limit ? -a.limit : u;
   }
-  return g * lin_sigmoid(a.alpha * g) * (u + a.beta);
+  return g * lin_sigmoid<FAST>(a.alpha * g) * (u + a.beta);
 }
 
 // d act / dz times dy
+template <bool FAST>
 __device__ __forceinline__ float lin_act_grad(float dy, float z, int act) {
   if (act == kActRelu) return z > 0.f ? dy : 0.f;
   if (act == kActGelu) {
     const float cdf = 0.5f * (1.f + erff(z * 0.70710678118654752f));
-    return dy * (cdf + z * 0.39894228040143268f * expf(-0.5f * z * z));
+    const float e = FAST ? __builtin_amdgcn_exp2f(z * z * -0.72134752044448170f) : expf(-0.5f * z * z);
+    return dy * (cdf + z * 0.39894228040143268f * e);
   }
   if (act == kActSilu) {
-    const float s = lin_sigmoid(z);
+    const float s = lin_sigmoid<FAST>(z);
     return dy * s * (1.f + z * (1.f - s));
   }
   return dy;
@@ -54,6 +66,7 @@ __device__ __forceinline__ float lin_act_grad(float dy, float z, int act) {
 
 // Gradients at gate and linear branch; a clamped value passes none (at the
 // bound itself it passes).
+template <bool FAST>
 __device__ __forceinline__ void lin_swiglu_grad(float dy, float g, float u, const LinearAct& a, float& dg, float& du) {
   bool gp = true, up = true;
   if (a.has_limit) {
@@ -62,7 +75,7 @@ __device__ __forceinline__ void lin_swiglu_grad(float dy, float g, float u, cons
     g = gp ? g : a.limit;
     u = u > a.limit ? a.limit : u < -a.limit ? -a.limit : u;
   }
-  const float s = lin_sigmoid(a.alpha * g);
+  const float s = lin_sigmoid<FAST>(a.alpha * g);
   dg = gp ? dy * (u + a.beta) * s * (1.f + a.alpha * g * (1.f - s)) : 0.f;
   du = up ? dy * g * s : 0.f;
 }
@@ -233,7 +246,7 @@ __device__ __forceinline__ void linear_rows(const LinearGemm& g, float (&z)[R][W
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
-      for (int i = 0; i < H; ++i) y[r][i] = lin_swiglu(z[r][2 * i], z[r][2 * i + 1], g.act);
+      for (int i = 0; i < H; ++i) y[r][i] = lin_swiglu<sizeof(ET) == 2>(z[r][2 * i], z[r][2 * i + 1], g.act);
     if (g.res) {
       const ET* res = static_cast<const ET*>(g.res) + (c >> 1);
       float v[R][H];
@@ -253,7 +266,7 @@ __device__ __forceinline__ void linear_rows(const LinearGemm& g, float (&z)[R][W
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
-      for (int i = 0; i < W; ++i) z[r][i] = lin_act(z[r][i], ACT);
+      for (int i = 0; i < W; ++i) z[r][i] = lin_act<sizeof(ET) == 2>(z[r][i], ACT);
     if (g.res) {
       const ET* res = static_cast<const ET*>(g.res) + c;
       float v[R][W];

@@ -118,10 +118,10 @@ __global__ void __launch_bounds__(256) qmoe_linear_act_grad(const LinearActGrad 
       float dz[W];
       if constexpr (glu) {
 #pragma unroll
-        for (int i = 0; i < H; ++i) lin_swiglu_grad(dy[r][i], z[r][2 * i], z[r][2 * i + 1], g.act, dz[2 * i], dz[2 * i + 1]);
+        for (int i = 0; i < H; ++i) lin_swiglu_grad<sizeof(ET) == 2>(dy[r][i], z[r][2 * i], z[r][2 * i + 1], g.act, dz[2 * i], dz[2 * i + 1]);
       } else {
 #pragma unroll
-        for (int i = 0; i < W; ++i) dz[i] = lin_act_grad(dy[r][i], z[r][i], ACT);
+        for (int i = 0; i < W; ++i) dz[i] = lin_act_grad<sizeof(ET) == 2>(dy[r][i], z[r][i], ACT);
       }
       // (columns from N on have a zero gradient: zeros in dz)
       if (g.dz && n < g.lddz) store_w<ET, W, VEC>(static_cast<ET*>(g.dz) + row * g.lddz + n, (int)g.lddz - n, dz);
