@@ -568,8 +568,9 @@ def _ok(status, where):
 
 
 def _ws(workspace, need, like):
-    """(pointer, bytes, tensor to keep until the call is enqueued) of a workspace of ``need`` bytes."""
-    if workspace is None:
+    """(pointer, bytes, tensor to keep until the call is enqueued) of a
+    workspace of ``need`` bytes: the one given if it is large enough."""
+    if workspace is None or workspace.numel() * workspace.element_size() < need:
         if need == 0:
             return None, 0, None
         workspace = like.new_empty(need, dtype=_uint8())

@@ -112,6 +112,7 @@ struct LinOperand {
                                        int lane) {
     ldb = (int)(ld * ES);
     const long at = kb * (RUN ? 128 : (long)BK * ldb);
+    if (RUN && rows > BT) rows = BT;  // (the tile's rows stay within 32 bits)
     base = reinterpret_cast<const char*>(src) + at;
     left = rows > 0 ? ((rows - 1) * ld + row_len) * ES - at : 0;
     if constexpr (RUN) {

@@ -152,7 +152,7 @@ qmoe_status check(const qmoe_tensor* input, const qmoe_tensor* weights, const qm
   // columns; the passes one per 256 columns of 64 rows
   const int64_t wide = std::max(p->N, p->K);
   if ((p->M / 32 + 9 + p->G) * (wide / 128 + 1) >= (int64_t(1) << 31) - 512 ||
-      (p->N / 32 + 1) * p->G * (p->K / 128 + 1) >= (int64_t(1) << 31) - 512)
+      ((p->N / 32 + 1) * p->G + 8) * (p->K / 128 + 1) >= (int64_t(1) << 31) - 512)
     return QMOE_ERR_UNSUPPORTED;
   p->type = T == QMOE_F32 ? LIN_F32 : T == QMOE_F16 ? LIN_F16 : LIN_BF16;
   p->es = T == QMOE_F32 ? 4 : 2;

@@ -266,3 +266,37 @@ def test_graph(torch, M):
         want = [*eager[0], *eager[1]] if i < 2 else [*run_forward(torch, c, a), *run_backward(torch, c, a)]
         for p, q in zip(want, (*f, *b)):
             assert torch.equal(p, q), i
+
+
+@pytest.mark.parametrize("dt", ["bfloat16", "float32"])
+def test_operands_beyond_two_gib(torch, dt):
+    # rows and weights whose byte offsets pass 31 bits, in every product; the reference in float64 on the GPU, a sample
+    # of the long side's rows (the sums of the weight gradient run over all of them)
+    M, K, N = (140000, 8192, 16) if dt == "bfloat16" else (70000, 8192, 16)
+    t = getattr(torch, dt)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    long = torch.randn(M, K, generator=g, device="cuda").to(t)
+    short = (torch.randn(N, K, generator=g, device="cuda") * K ** -0.5).to(t)
+    pick = torch.tensor([0, 1, 777, M // 2, M - 300, M - 257, M - 2, M - 1], device="cuda")
+    ref = long[pick].double() @ short.double().T
+    mag = long[pick].double().abs() @ short.double().abs().T
+    bound = lambda r, a, n: U.rounded(dt, U.back(r), U.sum_bound(n, U.back(a)))  # noqa: E731
+    y = qm.linear(long, short)
+    U.check(U.back(y[pick]), U.back(ref), bound(ref, mag, K), "long input")
+    y = qm.linear(short, long)
+    U.check(U.back(y[:, pick].T.contiguous()), U.back(ref), bound(ref, mag, K), "long weights")
+    dy = torch.randn(M, N, generator=g, device="cuda").to(t)
+    gi, gw, _ = qm.linear_backward(dy, long, short)
+    r, a = dy[pick].double() @ short.double(), dy[pick].double().abs() @ short.double().abs()
+    U.check(U.back(gi[pick]), U.back(r), bound(r, a, N), "grad_input")
+    r, a = torch.zeros(N, K, dtype=torch.float64, device="cuda"), torch.zeros(N, K, dtype=torch.float64, device="cuda")
+    for i in range(0, M, 20000):
+        d, x = dy[i:i + 20000].double().T.contiguous(), long[i:i + 20000].double()
+        r += d @ x
+        a += d.abs() @ x.abs()
+    U.check(U.back(gw), U.back(r), bound(r, a, M), "grad_weights")
+    dt2 = dy.T.contiguous()  # the long side as the columns of d
+    gi, gw, _ = qm.linear_backward(dt2, short, long)
+    U.check(U.back(gi), U.back(r), bound(r, a, M), "grad_input over long weights")
+    r, a = dy[pick].double() @ short.double(), dy[pick].double().abs() @ short.double().abs()
+    U.check(U.back(gw[pick]), U.back(r), bound(r, a, N), "long grad_weights")

@@ -196,6 +196,24 @@ def test_many_slots_over_many_blocks(torch):
     np.testing.assert_array_equal(inv.cpu().numpy().reshape(-1), np.where(flat < E, place, -1 - place))
 
 
+def test_rows_beyond_two_gib(torch):
+    T, H, k, E = 150000, 8192, 2, 8
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.randn(T, H, generator=g, device="cuda").bfloat16()
+    idx = torch.randint(0, E, (T, k), generator=g, device="cuda", dtype=torch.int32)
+    rows, off, perm, inv = qm.dispatch(x, idx, E)
+    pick = torch.tensor([0, 5, T - 1, T * k // 2, T * k - 300, T * k - 1], device="cuda")
+    assert torch.equal(rows[pick], x[perm[pick].long() // k])
+    w = torch.full((T, k), 0.5, device="cuda")
+    assert torch.equal(qm.combine(rows, inv, w), x)  # the halves of both copies
+    gr, gw = qm.combine_backward(x, rows, inv, w)
+    assert torch.equal(gr[pick], (x[perm[pick].long() // k].float() * 0.5).bfloat16())
+    tok = torch.tensor([0, T // 2, T - 1], device="cuda")
+    ref = (x[tok].double() ** 2).sum(1, keepdim=True).expand(-1, k)
+    U.check(U.back(gw[tok]), U.back(ref), U.sum_bound(H, U.back(ref)), "grad_weights")
+    assert torch.equal(qm.dispatch_backward(gr, inv), x)
+
+
 def test_no_tokens_no_slots_no_columns(torch):
     z = lambda *s: torch.empty(*s, device="cuda")  # noqa: E731
     i = lambda *s: torch.empty(*s, dtype=torch.int32, device="cuda")  # noqa: E731
