@@ -205,6 +205,8 @@ __global__ void __launch_bounds__(kSortRound) qmoe_sort_count(const void* __rest
 // the indices), then ranks 512 slots a round: lanes of one wavefront with the
 // same expert find each other with a ballot per bit of the expert's number,
 // wavefronts in order through LDS counts.
+// Bound by latency: 12288 slots of 64 experts take 7.2 us (11.4 us with four
+// loads in flight a thread and a second count of what comes before the chunk).
 __global__ void __launch_bounds__(kSortRound) qmoe_sort_place(const void* __restrict__ idx, bool idx64, int S, int E,
                                                               int chunk, int nchunks, const int* __restrict__ hist,
                                                               int* __restrict__ offsets, int* __restrict__ perm,
@@ -217,15 +219,26 @@ __global__ void __launch_bounds__(kSortRound) qmoe_sort_place(const void* __rest
   __shared__ int wsum[NW];
   const int lane = lane_id(), wave = threadIdx.x >> 6;
   const int s0 = blockIdx.x * chunk, s1 = min(S, s0 + chunk);
+  const int e0 = s0 + (int)threadIdx.x < s1 ? bucket(idx, idx64, s0 + threadIdx.x, E) : 0;
   if (!hist) {
     for (int e = threadIdx.x; e < 2 * B; e += kSortRound) sm[e] = 0;
     __syncthreads();
-    // (the whole array in base, what comes before the chunk in wcnt)
-#pragma unroll 4
-    for (int s = threadIdx.x; s < S; s += kSortRound) {
-      const int e = bucket(idx, idx64, s, E);
-      atomicAdd(&base[e], 1);
-      if (s < s0) atomicAdd(&wcnt[e], 1);
+    // (what comes before the chunk in wcnt, the rest in base; eight indices
+    // in flight a thread)
+    for (int s = threadIdx.x; s < S; s += 8 * kSortRound) {
+      int e[8];
+      if (idx64) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) e[j] = bucket(idx, true, min(s + j * kSortRound, S - 1), E);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) e[j] = bucket(idx, false, min(s + j * kSortRound, S - 1), E);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int at = s + j * kSortRound;
+        if (at < S) atomicAdd(&(at < s0 ? wcnt : base)[e[j]], 1);
+      }
     }
     __syncthreads();
   }
@@ -237,8 +250,8 @@ __global__ void __launch_bounds__(kSortRound) qmoe_sort_place(const void* __rest
     const int e = 2 * threadIdx.x + h;
     if (e >= B) continue;
     if (!hist) {
-      tot[h] = base[e];
       before[h] = wcnt[e];
+      tot[h] = base[e] + before[h];
     } else {
 #pragma unroll 8
       for (int c = 0; c < nchunks; ++c) {
@@ -274,7 +287,7 @@ __global__ void __launch_bounds__(kSortRound) qmoe_sort_place(const void* __rest
     __syncthreads();
     const int s = r0 + threadIdx.x;
     const bool valid = s < s1;
-    const int e = valid ? bucket(idx, idx64, s, E) : 0;
+    const int e = r0 == s0 ? e0 : valid ? bucket(idx, idx64, s, E) : 0;
     unsigned long long same = __ballot(valid);
     for (int b = 0; b < bits; ++b) {
       const unsigned long long m = __ballot((e >> b) & 1);
