@@ -13,7 +13,6 @@ namespace qmoe {
 typedef _Float16 h16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 b16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 // Activation codes (qmoe_activation of include/qmoe.h).
 constexpr int kActRelu = 0, kActSwiglu = 1, kActGelu = 2, kActSilu = 3, kActIdentity = 4;
@@ -184,11 +183,6 @@ template <typename ET>
 struct LinVec4 {
   typedef ET type __attribute__((ext_vector_type(4)));
 };
-template <typename ET>
-struct LinVec2 {
-  typedef ET type __attribute__((ext_vector_type(2)));
-};
-
 // W consecutive elements (W = 4 or 2; VEC: one access).
 template <typename ET, int W>
 struct LinVec {

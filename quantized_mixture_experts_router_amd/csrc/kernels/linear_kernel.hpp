@@ -149,6 +149,11 @@ struct LinOperand {
     base += step;
     left -= step;
   }
+  __device__ __forceinline__ void rewind(int stages) {
+    const long back = stages * (RUN ? 128 : (long)BK * ldb);
+    base -= back;
+    left += back;
+  }
 
   // This lane's operand of k step ks (32 16-bit or 16 32-bit r) for the 16
   // rows or columns from t0 on: r = 8 (lane / 16) .. + 7 of the step (32-bit:
@@ -197,7 +202,7 @@ __device__ __forceinline__ void tile_of(int b, int nq, int np, int& q, int& p) {
   p = r / h;
 }
 
-template <typename ET, int MODE, int BQ, int BP, int WQ, int WP, int NST, bool VEC>
+template <typename ET, int MODE, int BQ, int BP, int WQ, int WP, int NST, bool VEC, bool TURN>
 __global__ void __launch_bounds__(64 * WQ * WP) qmoe_linear(const LinearGemm g, int nq, int np) {
   constexpr int NW = WQ * WP, TQ = BQ / WQ / 16, TP = BP / WP / 16;
   using OP = LinOperand<ET, BP, MODE == LIN_FWD, NW>;
@@ -247,15 +252,23 @@ __global__ void __launch_bounds__(64 * WQ * WP) qmoe_linear(const LinearGemm g, 
   const int nk_all = (R + BK - 1) / BK;
   const int kb = (int)((long)nk_all * ks_id / g.splits);
   const int nk = (int)((long)nk_all * (ks_id + 1) / g.splits) - kb;
+  // TURN: the range is walked as a ring, every tile from its own stage on (the
+  // tiles of one q block together where those share much).  Rows that lie a
+  // power of two apart put a stage's pieces into few of the memory's channels,
+  // and tiles in step all ask for the same ones: one row by 28672 x 4096 takes
+  // 42 us turned and 51 us in step, 12288 rows in 64 groups by 2816 x 2048 283
+  // and 292 us.  Products of many dense tiles live on shared reads and lose
+  // 1 % to the bookkeeping.
+  int ka = TURN && nk > 0 ? kb + 5 * (BQ > 64 ? grp : grp + pb) % nk : kb;  // the stage to load next
   if constexpr (MODE == LIN_DW) {
-    op.init(static_cast<const ET*>(g.x) + (long)lo * g.ldx + p0, g.ldx, R, g.ldx - p0, g.K - p0, kb, wave, lane);
-    oq.init(static_cast<const ET*>(g.dz) + (long)lo * g.lddz + q0, g.lddz, R, g.lddz - q0, g.N - q0, kb, wave, lane);
+    op.init(static_cast<const ET*>(g.x) + (long)lo * g.ldx + p0, g.ldx, R, g.ldx - p0, g.K - p0, ka, wave, lane);
+    oq.init(static_cast<const ET*>(g.dz) + (long)lo * g.lddz + q0, g.lddz, R, g.lddz - q0, g.N - q0, ka, wave, lane);
   } else if constexpr (MODE == LIN_FWD) {
-    op.init(static_cast<const ET*>(g.w) + ((long)grp * g.N + p0) * g.ldw, g.ldw, g.N - p0, g.ldw, 0, kb, wave, lane);
-    oq.init(static_cast<const ET*>(g.x) + (long)lo * g.ldx, g.ldx, qrows, g.ldx, 0, kb, wave, lane);
+    op.init(static_cast<const ET*>(g.w) + ((long)grp * g.N + p0) * g.ldw, g.ldw, g.N - p0, g.ldw, 0, ka, wave, lane);
+    oq.init(static_cast<const ET*>(g.x) + (long)lo * g.ldx, g.ldx, qrows, g.ldx, 0, ka, wave, lane);
   } else {
-    op.init(static_cast<const ET*>(g.w) + (long)grp * g.N * g.ldw + p0, g.ldw, g.N, g.ldw - p0, g.K - p0, kb, wave, lane);
-    oq.init(static_cast<const ET*>(g.dz) + (long)lo * g.lddz, g.lddz, qrows, g.lddz, 0, kb, wave, lane);
+    op.init(static_cast<const ET*>(g.w) + (long)grp * g.N * g.ldw + p0, g.ldw, g.N, g.ldw - p0, g.K - p0, ka, wave, lane);
+    oq.init(static_cast<const ET*>(g.dz) + (long)lo * g.lddz, g.lddz, qrows, g.lddz, 0, ka, wave, lane);
   }
 
   f32x4 acc[TP][TQ];
@@ -265,8 +278,9 @@ __global__ void __launch_bounds__(64 * WQ * WP) qmoe_linear(const LinearGemm g, 
     for (int b = 0; b < TQ; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
   const int wq = wave / WP, wp = wave % WP;
   // float32: the sums of every kFold stages (256 r) are added up on their own,
-  // so that a long sum's error grows with its square root over 256 twice
-  // instead of once over all (8192 terms: 1.2e-6 -> 4e-7 of the result)
+  // which keeps a long sum's error at that of its pieces (root mean square of
+  // the error over the result's, normal operands, 1024 / 8192 / 32768 terms:
+  // 2.9e-7 / 3.0e-7 / 3.2e-7, in one sum 5.7e-7 / 1.1e-6 / 2.3e-6)
   constexpr int kFold = sizeof(ET) == 4 ? 8 : 0;
   f32x4 sum[kFold ? TP : 1][kFold ? TQ : 1];
   if constexpr (kFold > 0) {
@@ -291,11 +305,17 @@ __global__ void __launch_bounds__(64 * WQ * WP) qmoe_linear(const LinearGemm g, 
   // end zeros, so that the count of loads in flight stays the same.
   constexpr int kStage = OP::kLoads + OQ::kLoads;
   auto load = [&](int i, int kt, int u) QMOE_INLINE {
-    if (i < OP::kLoads) op.load(i, lds[u], (kb + kt) * BK, R, kt < nk, wave);
-    else oq.load(i - OP::kLoads, lds[u] + OP::kBytes, (kb + kt) * BK, R, kt < nk, wave);
+    const int at = TURN ? ka : kb + kt;
+    if (i < OP::kLoads) op.load(i, lds[u], at * BK, R, kt < nk, wave);
+    else oq.load(i - OP::kLoads, lds[u] + OP::kBytes, at * BK, R, kt < nk, wave);
     if (i == kStage - 1) {
       op.next();
       oq.next();
+      if (TURN && ++ka == kb + nk) {
+        ka = kb;
+        op.rewind(nk);
+        oq.rewind(nk);
+      }
     }
   };
   using Frag = typename LinMma<ET>::Frag;
@@ -471,8 +491,18 @@ hipError_t go_linear(const LinearGemm& g, bool vec, hipStream_t st) {
   const long h = nq < 8 ? nq : 8;
   const long share = ((nq + h - 1) / h * h * np + 7) / 8;
   const dim3 grid((unsigned)((share <= 32 ? share : (share + 31) / 32 * 32) * 8), (unsigned)g.splits), block(64 * WQ * WP);
-  if (vec) hipLaunchKernelGGL((qmoe_linear<ET, MODE, BQ, BP, WQ, WP, NST, true>), grid, block, 0, st, g, (int)nq, (int)np);
-  else hipLaunchKernelGGL((qmoe_linear<ET, MODE, BQ, BP, WQ, WP, NST, false>), grid, block, 0, st, g, (int)nq, (int)np);
+  auto go = [&](auto v, auto t) {
+    hipLaunchKernelGGL((qmoe_linear<ET, MODE, BQ, BP, WQ, WP, NST, decltype(v)::value, decltype(t)::value>), grid, block,
+                       0, st, g, (int)nq, (int)np);
+  };
+  auto turned = [&](auto t) { vec ? go(std::true_type{}, t) : go(std::false_type{}, t); };
+  if constexpr (MODE == LIN_FWD) {
+    if (g.offsets || nq == 1) {
+      turned(std::true_type{});
+      return hipGetLastError();
+    }
+  }
+  turned(std::false_type{});
   return hipGetLastError();
 }
 
