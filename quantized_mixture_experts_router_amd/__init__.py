@@ -487,14 +487,14 @@ _code_of = {}  # torch dtype -> code, filled as types are met
 _tls = threading.local()
 
 
-def _pack(ts):
+def _pack(ts, first=0):
     """Addresses (None for None) of the tensors' descriptors in this thread's
-    buffer, valid until its next _pack."""
+    buffer from place ``first`` on, valid until its next _pack of that place."""
     buf = getattr(_tls, "buf", None)
     if buf is None:
         buf = _tls.buf = ctypes.create_string_buffer(40 * len(_FMT))
         _tls.at = ctypes.addressof(buf)
-    vals, out, at = [], [], _tls.at
+    vals, out, at = [], [], _tls.at + 40 * first
     for t in ts:
         if t is None:
             vals += (0, 0, 0, 0, 0, 0)
@@ -518,7 +518,7 @@ def _pack(ts):
                 vals += (ptr, code, r, d[0], d[1], d[2])
             out.append(at)
         at += 40
-    _FMT[len(ts)].pack_into(buf, 0, *vals)
+    _FMT[len(ts)].pack_into(buf, 40 * first, *vals)
     return out
 
 
@@ -665,7 +665,7 @@ def dispatch(input, indices, experts, stream=None, workspace=None):
         perm = indices.new_empty(T * k, dtype=torch.int32)
         inverse = indices.new_empty((T, k), dtype=torch.int32)
         w, n, _keep = _ws(workspace, need.value, input)
-        x, i, r, o, p, v = _pack((input, indices, rows, offsets, perm, inverse))
+        r, o, p, v = _pack((rows, offsets, perm, inverse), 2)
         _ok(lib.qmoe_dispatch(x, i, int(experts), r, o, p, v, w, n, st), "qmoe_dispatch")
     return rows, offsets, perm, inverse
 

