@@ -27,6 +27,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 import struct
 import threading
@@ -480,11 +481,15 @@ def moe_forward(tensors: dict, attrs=None, stream=None, workspace=None, output=N
 # These calls are small next to their launches, so their arguments are packed
 # at once: every tensor's qmoe_tensor lies in one buffer per thread, which the
 # library reads during the call only.
-_FMT = [struct.Struct("=" + "qiiqqq" * n) for n in range(12)]
+_ONE = struct.Struct("=qiiqqq").pack_into
 _CODES = {"float32": QMOE_F32, "uint8": QMOE_U8, "int32": QMOE_I32, "int64": QMOE_I64, "float16": QMOE_F16,
           "bfloat16": QMOE_BF16, "float64": QMOE_F64}
 _code_of = {}  # torch dtype -> code, filled as types are met
 _tls = threading.local()
+
+
+def _type_code(dtype):
+    return _CODES.get(str(dtype).replace("torch.", ""), 0)
 
 
 def _pack(ts, first=0):
@@ -492,33 +497,33 @@ def _pack(ts, first=0):
     buffer from place ``first`` on, valid until its next _pack of that place."""
     buf = getattr(_tls, "buf", None)
     if buf is None:
-        buf = _tls.buf = ctypes.create_string_buffer(40 * len(_FMT))
+        buf = _tls.buf = ctypes.create_string_buffer(40 * 12)
         _tls.at = ctypes.addressof(buf)
-    vals, out, at = [], [], _tls.at + 40 * first
+    at, off, out = _tls.at, 40 * first, []
     for t in ts:
         if t is None:
-            vals += (0, 0, 0, 0, 0, 0)
             out.append(None)
         else:
             dt = t.dtype
             code = _code_of.get(dt)
-            if code is None:
-                code = _code_of[dt] = _CODES.get(str(dt).replace("torch.", ""), 0)
-            shape = t.shape
-            r = len(shape)
-            ptr = 0
-            if hasattr(t, "data_ptr"):
+            if code is not None or hasattr(t, "data_ptr"):
+                if code is None:
+                    code = _code_of[dt] = _type_code(dt)
                 if not t.is_contiguous():
                     raise ValueError("qmoe tensors must be contiguous")
                 ptr = t.data_ptr()
+            else:  # an array of another kind: extents and type only
+                code, ptr = _type_code(dt), 0
+            shape = t.shape
+            r = len(shape)
             if r == 2:
-                vals += (ptr, code, 2, shape[0], shape[1], 0)
+                d0, d1 = shape
+                _ONE(buf, off, ptr, code, 2, d0, d1, 0)
             else:
                 d = tuple(shape[:3]) + (0, 0, 0)
-                vals += (ptr, code, r, d[0], d[1], d[2])
-            out.append(at)
-        at += 40
-    _FMT[len(ts)].pack_into(buf, 40 * first, *vals)
+                _ONE(buf, off, ptr, code, r, d[0], d[1], d[2])
+            out.append(at + off)
+        off += 40
     return out
 
 
@@ -543,10 +548,19 @@ class _Stream:
 _NOTHING = contextlib.nullcontext()
 
 
+@functools.cache
+def _current():
+    """(current device's index, handle of a device's current stream): the handle
+    straight from torch where it offers that, without the 1 us that building a
+    Stream object takes of a 10 us call."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return torch.cuda.current_device, raw or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _on(stream, ts):
     """(context, stream handle) of a call on these tensors, which lie on one
     GPU: its current stream unless ``stream`` is given."""
-    import torch
     dev = None
     for t in ts:
         if t is not None:
@@ -558,8 +572,9 @@ def _on(stream, ts):
                                  f"{sorted({str(u.device) for u in ts if u is not None})}")
     if stream is not None and stream.device.index != dev:
         raise ValueError(f"stream of {stream.device}, tensors on cuda:{dev}")
-    ctx = _NOTHING if stream is None and dev == torch.cuda.current_device() else _Stream(dev, stream)
-    return ctx, (torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream
+    device, handle = _current()
+    ctx = _NOTHING if stream is None and dev == device() else _Stream(dev, stream)
+    return ctx, handle(dev) if stream is None else stream.cuda_stream
 
 
 def _ok(status, where):
