@@ -252,14 +252,16 @@ __global__ void __launch_bounds__(64 * WQ * WP) qmoe_linear(const LinearGemm g, 
   const int nk_all = (R + BK - 1) / BK;
   const int kb = (int)((long)nk_all * ks_id / g.splits);
   const int nk = (int)((long)nk_all * (ks_id + 1) / g.splits) - kb;
-  // TURN: the range is walked as a ring, every tile from its own stage on (the
-  // tiles of one q block together where those share much).  Rows that lie a
+  // TURN: the range is walked as a ring, every group's tiles from a stage of
+  // their own on (in a product of one q block every tile).  Rows that lie a
   // power of two apart put a stage's pieces into few of the memory's channels,
   // and tiles in step all ask for the same ones: one row by 28672 x 4096 takes
-  // 42 us turned and 51 us in step, 12288 rows in 64 groups by 2816 x 2048 283
-  // and 292 us.  Products of many dense tiles live on shared reads and lose
-  // 1 % to the bookkeeping.
-  int ka = TURN && nk > 0 ? kb + 5 * (BQ > 64 ? grp : grp + pb) % nk : kb;  // the stage to load next
+  // 41 us turned and 51 us in step, 128 rows 65 and 71 us, 12288 rows in 64
+  // groups by 2816 x 2048 279 and 292 us.  A group's tiles stay in step, since
+  // they share its rows (8 groups of 64 rows by 14336 x 4096: 182 us, 188 us with
+  // every tile on its own); so do all tiles of other dense products, which
+  // would lose 1 % to the bookkeeping.
+  int ka = TURN && nk > 0 ? kb + 5 * (g.offsets ? grp : pb) % nk : kb;  // the stage to load next
   if constexpr (MODE == LIN_DW) {
     op.init(static_cast<const ET*>(g.x) + (long)lo * g.ldx + p0, g.ldx, R, g.ldx - p0, g.K - p0, ka, wave, lane);
     oq.init(static_cast<const ET*>(g.dz) + (long)lo * g.lddz + q0, g.lddz, R, g.lddz - q0, g.N - q0, ka, wave, lane);
