@@ -287,10 +287,15 @@ __host__ __device__ __forceinline__ void with_act(int act, F f) {
   }
 }
 
-// Zeros where the epilogue of the same columns would write (rows behind the
-// last group).
-template <typename ET>
+// Zeros in the four columns from n on of row m (behind the last group), as the
+// product (MODE) would write them.
+template <typename ET, int MODE>
 __device__ __forceinline__ void linear_zero(const LinearGemm& g, int m, int n) {
+  if constexpr (MODE != LIN_FWD) {
+    const float z[4] = {};
+    store_w<ET, 4, false>(static_cast<ET*>(g.out) + (long)m * g.K + n, g.K - n, z);
+    return;
+  }
   const bool glu = g.act.type == kActSwiglu;
   const long No = glu ? g.N >> 1 : g.N;
 #pragma unroll
@@ -299,22 +304,6 @@ __device__ __forceinline__ void linear_zero(const LinearGemm& g, int m, int n) {
     if (g.pre) static_cast<ET*>(g.pre)[(long)m * g.N + n + i] = (ET)0.f;
     if (!glu) static_cast<ET*>(g.out)[(long)m * No + n + i] = (ET)0.f;
     else if (i % 2 == 0) static_cast<ET*>(g.out)[(long)m * No + ((n + i) >> 1)] = (ET)0.f;
-  }
-}
-
-// Four consecutive columns of a gradient row of `cols` columns.
-template <typename ET, bool VEC>
-__device__ __forceinline__ void store_cols4(ET* row, int c, int cols, f32x4 v) {
-  if (c >= cols) return;
-  if constexpr (VEC) {
-    typename LinVec<ET, 4>::type t;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) t[i] = (ET)v[i];
-    *(typename LinVec<ET, 4>::type*)(row + c) = t;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (c + i < cols) row[c + i] = (ET)v[i];
   }
 }
 

@@ -241,8 +241,7 @@ __global__ void __launch_bounds__(64 * WQ * WP) qmoe_linear(const LinearGemm g, 
       if (ks_id > 0 || g.splits > 1) return;  // (the finishing pass writes them)
       for (int i = threadIdx.x; i < min(qrows, BQ) * (BP / 4); i += 64 * NW) {
         const int m = q0 + i / (BP / 4), c = p0 + 4 * (i % (BP / 4));
-        if constexpr (MODE == LIN_FWD) linear_zero<ET>(g, m, c);
-        else store_cols4<ET, false>(static_cast<ET*>(g.out) + (long)m * g.K, c, g.K, f32x4{0.f, 0.f, 0.f, 0.f});
+        linear_zero<ET, MODE>(g, m, c);
       }
       return;
     }

@@ -24,46 +24,57 @@ __device__ __forceinline__ int group_of_row(const int* __restrict__ offsets, int
   return a;
 }
 
-// Four columns of one output row a thread: the ranges' sums added in range
-// order, then the epilogue (or the store).  1001 x 1411 float32, two ranges,
-// gelu, pre-activations kept: 9.8 us for 23 MB, 5 us of it the copy's rate.
+// Four columns of one output row a thread (two where rows allow no wide
+// access): the ranges' sums added in range order, then the epilogue (or the
+// store).  1001 x 1411 float32, two ranges, gelu, pre-activations kept: 7.2 us for
+// 23 MB (9.8 us with four columns a thread, whose single stores then lie 16 bytes
+// apart).
 template <typename ET, int MODE, bool VEC>
 __global__ void __launch_bounds__(256) qmoe_linear_finish(const LinearGemm g) {
+  constexpr int W = VEC ? 4 : 2;
+  typedef float V __attribute__((ext_vector_type(W)));
   const int cols = MODE == LIN_FWD ? g.N : g.K;
   const long ldp = (cols + 3) & ~3;
   const long rows = MODE == LIN_DW ? (long)g.G * g.N : g.M;
-  const long i = (long)blockIdx.x * 256 + threadIdx.x;
-  const long row = i / (ldp >> 2);
-  const int c = (int)(i - row * (ldp >> 2)) * 4;
+  // (fewer than 2^31 outputs where a reduction is split)
+  const uint32_t i = blockIdx.x * 256 + threadIdx.x, per = (uint32_t)ldp / W;
+  const long row = i / per;
+  const int c = (int)(i - (uint32_t)row * per) * W;
   if (row >= rows) return;
   int grp = 0;
   if constexpr (MODE != LIN_DW) {
     grp = group_of_row(g.offsets, g.G, g.M, (int)row);
     if (grp >= g.G) {
-      if constexpr (MODE == LIN_FWD) linear_zero<ET>(g, (int)row, c);
-      else store_cols4<ET, false>(static_cast<ET*>(g.out) + row * g.K, c, g.K, f32x4{0.f, 0.f, 0.f, 0.f});
+      if (c % 4 != 0) return;
+      linear_zero<ET, MODE>(g, (int)row, c);
       return;
     }
   }
-  f32x4 v = {0.f, 0.f, 0.f, 0.f};
-  for (int s = 0; s < g.splits; ++s) v += *(const f32x4*)(g.partial + (s * rows + row) * ldp + c);
+  float z[1][W] = {};
+#pragma unroll 4
+  for (int s = 0; s < g.splits; ++s) {
+    const V v = *(const V*)(g.partial + (s * rows + row) * ldp + c);
+#pragma unroll
+    for (int j = 0; j < W; ++j) z[0][j] += v[j];
+  }
   if constexpr (MODE == LIN_FWD) {
-    float z[1][4] = {{v[0], v[1], v[2], v[3]}}, b[4] = {};
+    float b[W] = {};
     const int m[1] = {(int)row};
     const bool ok[1] = {true};
     if (c >= g.N) return;
-    if (g.bias) load_w<ET, 4, VEC>(static_cast<const ET*>(g.bias) + (long)grp * g.N + c, g.N - c, b);
-    with_act(g.act.type, [&](auto act) { linear_rows<ET, decltype(act)::value, 4, 1, VEC>(g, z, b, c, m, ok); });
-  } else store_cols4<ET, VEC>(static_cast<ET*>(g.out) + row * g.K, c, g.K, v);
+    if (g.bias) load_w<ET, W, VEC>(static_cast<const ET*>(g.bias) + (long)grp * g.N + c, g.N - c, b);
+    with_act(g.act.type, [&](auto act) { linear_rows<ET, decltype(act)::value, W, 1, VEC>(g, z, b, c, m, ok); });
+  } else if (c < g.K) store_w<ET, W, VEC>(static_cast<ET*>(g.out) + row * g.K + c, g.K - c, z[0]);
 }
 
 template <typename ET, int MODE>
 hipError_t go_finish(const LinearGemm& g, hipStream_t st) {
   const long cols = MODE == LIN_FWD ? g.N : g.K;
   const long rows = MODE == LIN_DW ? (long)g.G * g.N : g.M;
-  const long n = rows * ((cols + 3) / 4);
+  const bool vec = linear_vec<ET>(g, MODE);
+  const long n = rows * ((cols + 3) / 4) * (vec ? 1 : 2);
   const dim3 grid((unsigned)((n + 255) / 256)), block(256);
-  if (linear_vec<ET>(g, MODE)) hipLaunchKernelGGL((qmoe_linear_finish<ET, MODE, true>), grid, block, 0, st, g);
+  if (vec) hipLaunchKernelGGL((qmoe_linear_finish<ET, MODE, true>), grid, block, 0, st, g);
   else hipLaunchKernelGGL((qmoe_linear_finish<ET, MODE, false>), grid, block, 0, st, g);
   return hipGetLastError();
 }

@@ -67,6 +67,7 @@ LinearPlan plan_product(int type, int64_t rows, int64_t groups, int64_t cols, in
     const int64_t n = ceil_div(per, t.bq) * std::min(groups, rows) * ceil_div(cols, t.bp);
     for (int64_t s : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
       if (s > 1 && stages < 4 * s) break;  // at least four stages a range
+      if (s > 1 && rows * (cols + 3) >= int64_t(1) << 31) break;  // (the finishing pass counts outputs in 32 bits)
       // (alone on its compute unit a float32 item leaves the matrix cores a fifth idle)
       const double slow = type == LIN_F32 && n * s <= cus ? 1.2 : 1.0;
       double cost = (double)ceil_div(n * s, cus) * (t.fixed + (double)ceil_div(stages, s) * stage * slow);
