@@ -539,6 +539,8 @@ void qmoe_linear_attrs_default(qmoe_linear_attrs* a);
  * Products: T float32, float32 matrix instructions; float16 and bfloat16,
  * exact products of the 16-bit values summed in float32.  A long reduction
  * over few rows is cut into ranges whose float32 sums are added in order.
+ * The order of an output's terms depends on the sizes and on its group and
+ * column, so a row's bits may differ between calls of other sizes or groups.
  * input and weights 16-byte aligned when K is a whole number of 16-byte runs
  * (else they are first copied to padded rows in the workspace).
  * G <= 1023, M <= 2^30, K and N <= 2^20 (QMOE_ERR_UNSUPPORTED).

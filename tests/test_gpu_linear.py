@@ -300,3 +300,18 @@ def test_operands_beyond_two_gib(torch, dt):
     U.check(U.back(gi), U.back(r), bound(r, a, M), "grad_input over long weights")
     r, a = dy[pick].double() @ short.double(), dy[pick].double().abs() @ short.double().abs()
     U.check(U.back(gw[pick]), U.back(r), bound(r, a, N), "long grad_weights")
+
+
+RINGS = [(5, 1000, 4100, None),             # one q block, a column block a start, a last stage that is not whole
+         (3, 8200, 260, None),              # ranges of the reduction, each a ring of its own
+         (2, 40, 1290, None),               # one stage: every start is the same
+         (90, 456, 131, [2] * 45),          # more groups than stages, rows that allow no wide access
+         (300, 1544, 200, [1, 0, 290] + [3] * 3)]
+
+
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("M,K,N,counts", RINGS)
+def test_starts_of_the_reduction(torch, dt, M, K, N, counts):
+    for kind, a in (("gelu", {}), ("identity", {})):
+        c = make(torch, dt, M, K, N, counts, kind, residual=True, seed=M + K)
+        check_forward(torch, c, dt, kind, a, f"M={M} K={K} N={N} groups={0 if counts is None else len(counts)} {kind}")
