@@ -7,6 +7,7 @@
 
 #include "common.hpp"
 #include "linear.h"
+#include "linear_tiles.h"
 
 namespace qmoe {
 

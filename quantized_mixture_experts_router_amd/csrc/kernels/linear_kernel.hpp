@@ -189,19 +189,6 @@ struct LinOperand {
   }
 };
 
-// Output tiles are taken in runs of up to 32 per XCD (workgroups go to the 8
-// XCDs in turn; 32 compute units each; every XCD gets the same number of runs),
-// inside a run eight q blocks by four p blocks, so that a run's operand rows
-// are shared in its XCD's L2.
-__device__ __forceinline__ void tile_of(int b, int nq, int np, int& q, int& p) {
-  const int h = min(nq, 8);
-  const int share = ((nq + h - 1) / h * h * np + 7) >> 3, runs = (share + 31) >> 5, run = (share + runs - 1) / runs;
-  const int t = ((b >> 3) / run * 8 + (b & 7)) * run + (b >> 3) % run;
-  const int s = t / (h * np), r = t - s * (h * np);
-  q = s * h + r % h;
-  p = r / h;
-}
-
 template <typename ET, int MODE, int BQ, int BP, int WQ, int WP, int NST, bool VEC, bool TURN>
 __global__ void __launch_bounds__(64 * WQ * WP) qmoe_linear(const LinearGemm g, int nq, int np) {
   constexpr int NW = WQ * WP, TQ = BQ / WQ / 16, TP = BP / WP / 16;
@@ -211,13 +198,15 @@ __global__ void __launch_bounds__(64 * WQ * WP) qmoe_linear(const LinearGemm g, 
   __shared__ __attribute__((aligned(1024))) char lds[NST][OP::kBytes + OQ::kBytes];
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
-  int qb, pb;
   const int ks_id = blockIdx.y;  // range of r
-  // (in rows of groups only the device knows how many blocks there are)
+  // (in rows of groups only the device knows how many blocks there are; falling
+  // offsets make groups overlap, and the host's bound keeps the walk over
+  // the tiles within 32 bits)
   const RowBlocks blocks(MODE == LIN_DW ? nullptr : g.offsets, g.G, g.M, BQ);
-  if (MODE != LIN_DW && g.offsets) nq = blocks.total;
+  if (MODE != LIN_DW && g.offsets) nq = min(blocks.total, nq);
   if (nq <= 0) return;
-  tile_of(blockIdx.x, nq, np, qb, pb);
+  const LinearTileAt tile = linear_tile_of(blockIdx.x, nq, np);
+  const int qb = tile.q, pb = tile.p;
   const int p0 = pb * BP;
   int grp, lo, hi, q0, qrows;  // group, its rows from the tile on, first output row, valid rows of the tile
   const int pcols = MODE == LIN_FWD ? g.N : g.K;
@@ -487,11 +476,7 @@ hipError_t go_linear(const LinearGemm& g, bool vec, hipStream_t st) {
   const long qb = (rows + BQ - 1) / BQ;
   const long nq = MODE == LIN_DW ? qb * g.G : g.offsets ? qb + g.G + 1 : qb;
   const long np = (cols + BP - 1) / BP;
-  // workgroups for the most tiles there can be (tile_of's runs cover at most
-  // these)
-  const long h = nq < 8 ? nq : 8;
-  const long share = ((nq + h - 1) / h * h * np + 7) / 8;
-  const dim3 grid((unsigned)((share <= 32 ? share : (share + 31) / 32 * 32) * 8), (unsigned)g.splits), block(64 * WQ * WP);
+  const dim3 grid((unsigned)linear_workgroups(nq, np), (unsigned)g.splits), block(64 * WQ * WP);
   auto go = [&](auto v, auto t) {
     hipLaunchKernelGGL((qmoe_linear<ET, MODE, BQ, BP, WQ, WP, NST, decltype(v)::value, decltype(t)::value>), grid, block,
                        0, st, g, (int)nq, (int)np);

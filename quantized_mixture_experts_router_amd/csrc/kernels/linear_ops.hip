@@ -186,7 +186,8 @@ __global__ void __launch_bounds__(256) qmoe_linear_bias_grad(const float* __rest
   const int grp = blockIdx.x / ncol;
   int first, count;
   group_blocks(offsets, G, M, kSumRows, grp, first, count);
-  count = max(0, min(count, nblocks - first));  // (falling offsets)
+  // (falling offsets: groups overlap, their blocks pass what there is or 31 bits)
+  count = first < 0 ? 0 : max(0, min(count, nblocks - first));
   const int n = (blockIdx.x % ncol) * 256 + threadIdx.x;
   if (n >= N) return;
   float s = 0.f;
