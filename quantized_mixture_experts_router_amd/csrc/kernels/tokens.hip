@@ -7,6 +7,7 @@
 // every output element has one writer, so results do not depend on order.
 #include <math.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "common.hpp"
@@ -39,8 +40,9 @@ __device__ __forceinline__ int read_index(const void* idx, bool idx64, long i) {
 // logits: 2.6 us).
 template <int V>
 __global__ void __launch_bounds__(256) qmoe_route_topk(const float* __restrict__ logits, int T, int E, int k,
-                                                       bool over_all, int* __restrict__ idx, float* __restrict__ w) {
-  const int t = blockIdx.x * 4 + (threadIdx.x >> 6), lane = lane_id();
+                                                       bool over_all, int b0, int* __restrict__ idx,
+                                                       float* __restrict__ w) {
+  const int t = (b0 + blockIdx.x) * 4 + (threadIdx.x >> 6), lane = lane_id();
   if (t >= T) return;
   const float* row = logits + (long)t * E;
   float v[V];
@@ -115,12 +117,12 @@ __global__ void __launch_bounds__(256) qmoe_route_topk(const float* __restrict__
 template <int V>
 __global__ void __launch_bounds__(256) qmoe_route_grad(const float* __restrict__ gw, const float* __restrict__ logits,
                                                        const void* __restrict__ idx, bool idx64, int T, int E, int k,
-                                                       bool over_all, float* __restrict__ gl) {
+                                                       bool over_all, int b0, float* __restrict__ gl) {
   extern __shared__ char smem[];  // per wavefront: k experts, k values
   const int wave = threadIdx.x >> 6, lane = lane_id();
   int* se = reinterpret_cast<int*>(smem) + wave * 2 * k;
   float* sv = reinterpret_cast<float*>(se + k);
-  const int t = blockIdx.x * 4 + wave;
+  const int t = (b0 + blockIdx.x) * 4 + wave;
   if (t >= T) return;
   const float* row = logits + (long)t * E;
   float v[V];
@@ -344,8 +346,9 @@ __device__ __forceinline__ void piece_set(typename Piece<ET, WIDE>::type& p, int
 // to 6 places each (59 MB) in 10.4 us, 5.6 TB/s.
 template <typename U>
 __global__ void __launch_bounds__(256) qmoe_dispatch_rows(const U* __restrict__ x, const int* __restrict__ inverse,
-                                                          int T, int k, long pieces, int per_log, U* __restrict__ rows) {
-  const long t = ((long)blockIdx.x << (8 - per_log)) + (threadIdx.x >> per_log);
+                                                          int T, int k, long pieces, int per_log, int b0,
+                                                          U* __restrict__ rows) {
+  const long t = ((long)(b0 + blockIdx.x) << (8 - per_log)) + (threadIdx.x >> per_log);
   const long c = ((long)blockIdx.y << per_log) + (threadIdx.x & ((1 << per_log) - 1));
   if (t >= T || c >= pieces) return;
   const U v = x[t * pieces + c];
@@ -362,10 +365,10 @@ __global__ void __launch_bounds__(256) qmoe_dispatch_rows(const U* __restrict__ 
 template <typename ET, bool WIDE>
 __global__ void __launch_bounds__(256) qmoe_combine_rows(const ET* __restrict__ rows, const int* __restrict__ inverse,
                                                          const float* __restrict__ w, int T, int k, long pieces,
-                                                         int per_log, ET* __restrict__ out) {
+                                                         int per_log, int b0, ET* __restrict__ out) {
   using P = Piece<ET, WIDE>;
   using V = typename P::type;
-  const long t = ((long)blockIdx.x << (8 - per_log)) + (threadIdx.x >> per_log);
+  const long t = ((long)(b0 + blockIdx.x) << (8 - per_log)) + (threadIdx.x >> per_log);
   const long c = ((long)blockIdx.y << per_log) + (threadIdx.x & ((1 << per_log) - 1));
   if (t >= T || c >= pieces) return;
   const V* src = reinterpret_cast<const V*>(rows) + c;
@@ -404,11 +407,11 @@ __global__ void __launch_bounds__(256) qmoe_combine_rows(const ET* __restrict__ 
 template <typename ET, bool WIDE>
 __global__ void __launch_bounds__(256) qmoe_combine_grad(const ET* __restrict__ gout, const ET* __restrict__ rows,
                                                          const int* __restrict__ inverse, const float* __restrict__ w,
-                                                         int S, int k, long pieces, ET* __restrict__ grows,
+                                                         int S, int k, long pieces, int b0, ET* __restrict__ grows,
                                                          float* __restrict__ gw) {
   using P = Piece<ET, WIDE>;
   using V = typename P::type;
-  const long s = (long)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const long s = (long)(b0 + blockIdx.x) * 4 + (threadIdx.x >> 6);
   if (s >= S) return;
   const int lane = lane_id();
   const int p = inverse[s];
@@ -456,13 +459,32 @@ bool wide_ok(long row_bytes, std::initializer_list<const void*> ps) {
   return true;
 }
 
-// Threads a token (log2) and the grid for rows of `pieces`.
-dim3 row_grid(long T, long pieces, int* per_log) {
+// One dimension of a launch holds fewer than 2^32 threads: `blocks` workgroups
+// of 256 in launches of 2^23 at most, f(first, count) each (2^26 tokens of the
+// router, 2^24 of long rows are the first that need two).
+constexpr long kMaxLaunch = 1l << 23;
+template <typename F>
+hipError_t in_launches(long blocks, F f) {
+  for (long b = 0; b < blocks; b += kMaxLaunch) {
+    f((int)b, (unsigned)std::min(blocks - b, kMaxLaunch));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+// Threads a token (log2) and the grid for rows of `pieces`: workgroups of
+// tokens in x, of pieces in y.
+struct RowGrid {
+  int per_log;
+  long x;
+  unsigned y;
+};
+RowGrid row_grid(long T, long pieces) {
   int l = 0;
   while (l < 8 && (1l << l) < pieces) ++l;
-  *per_log = l;
   const long tb = 1l << (8 - l);
-  return dim3((unsigned)((T + tb - 1) / tb), (unsigned)((pieces + (1l << l) - 1) >> l));
+  return {l, (T + tb - 1) / tb, (unsigned)((pieces + (1l << l) - 1) >> l)};
 }
 
 template <typename ET>
@@ -470,13 +492,14 @@ hipError_t combine_rows_t(const void* rows, const int* inverse, const float* w, 
                           hipStream_t st) {
   const bool wide = wide_ok(H * (long)sizeof(ET), {rows, out});
   const long pieces = wide ? H * (long)sizeof(ET) / 16 : H;
-  int pl;
-  const dim3 grid = row_grid(T, pieces, &pl), block(256);
-  if (wide)
-    hipLaunchKernelGGL((qmoe_combine_rows<ET, true>), grid, block, 0, st, (const ET*)rows, inverse, w, T, k, pieces, pl, (ET*)out);
-  else
-    hipLaunchKernelGGL((qmoe_combine_rows<ET, false>), grid, block, 0, st, (const ET*)rows, inverse, w, T, k, pieces, pl, (ET*)out);
-  return hipGetLastError();
+  const RowGrid r = row_grid(T, pieces);
+  return in_launches(r.x, [&](int b0, unsigned n) {
+    const dim3 grid(n, r.y), block(256);
+    if (wide)
+      hipLaunchKernelGGL((qmoe_combine_rows<ET, true>), grid, block, 0, st, (const ET*)rows, inverse, w, T, k, pieces, r.per_log, b0, (ET*)out);
+    else
+      hipLaunchKernelGGL((qmoe_combine_rows<ET, false>), grid, block, 0, st, (const ET*)rows, inverse, w, T, k, pieces, r.per_log, b0, (ET*)out);
+  });
 }
 
 template <typename ET>
@@ -485,12 +508,13 @@ hipError_t combine_grad_t(const void* gout, const void* rows, const int* inverse
   const bool wide = wide_ok(H * (long)sizeof(ET), {gout, rows, grows});
   const long pieces = wide ? H * (long)sizeof(ET) / 16 : H;
   const int S = T * k;
-  const dim3 grid((unsigned)((S + 3) / 4)), block(256);
-  if (wide)
-    hipLaunchKernelGGL((qmoe_combine_grad<ET, true>), grid, block, 0, st, (const ET*)gout, (const ET*)rows, inverse, w, S, k, pieces, (ET*)grows, gw);
-  else
-    hipLaunchKernelGGL((qmoe_combine_grad<ET, false>), grid, block, 0, st, (const ET*)gout, (const ET*)rows, inverse, w, S, k, pieces, (ET*)grows, gw);
-  return hipGetLastError();
+  return in_launches((S + 3) / 4, [&](int b0, unsigned n) {
+    const dim3 grid(n), block(256);
+    if (wide)
+      hipLaunchKernelGGL((qmoe_combine_grad<ET, true>), grid, block, 0, st, (const ET*)gout, (const ET*)rows, inverse, w, S, k, pieces, b0, (ET*)grows, gw);
+    else
+      hipLaunchKernelGGL((qmoe_combine_grad<ET, false>), grid, block, 0, st, (const ET*)gout, (const ET*)rows, inverse, w, S, k, pieces, b0, (ET*)grows, gw);
+  });
 }
 
 }  // namespace
@@ -508,22 +532,25 @@ hipError_t combine_grad_t(const void* gout, const void* rows, const int* inverse
 
 hipError_t launch_route_topk(const float* logits, int T, int E, int k, bool over_all, int* idx, float* w,
                              hipStream_t st) {
-  const dim3 grid((T + 3) / 4), block(256);
-#define QMOE_CALL(VV) hipLaunchKernelGGL(qmoe_route_topk<VV>, grid, block, 0, st, logits, T, E, k, over_all, idx, w)
-  QMOE_BY_REGS(QMOE_CALL)
+  return in_launches((T + 3) / 4, [&](int b0, unsigned n) {
+    const dim3 grid(n), block(256);
+#define QMOE_CALL(VV) \
+  hipLaunchKernelGGL(qmoe_route_topk<VV>, grid, block, 0, st, logits, T, E, k, over_all, b0, idx, w)
+    QMOE_BY_REGS(QMOE_CALL)
 #undef QMOE_CALL
-  return hipGetLastError();
+  });
 }
 
 hipError_t launch_route_grad(const float* gw, const float* logits, const void* idx, bool idx64, int T, int E, int k,
                              bool over_all, float* gl, hipStream_t st) {
-  const dim3 grid((T + 3) / 4), block(256);
   const size_t lds = (size_t)4 * 2 * k * 4;
+  return in_launches((T + 3) / 4, [&](int b0, unsigned n) {
+    const dim3 grid(n), block(256);
 #define QMOE_CALL(VV) \
-  hipLaunchKernelGGL(qmoe_route_grad<VV>, grid, block, lds, st, gw, logits, idx, idx64, T, E, k, over_all, gl)
-  QMOE_BY_REGS(QMOE_CALL)
+  hipLaunchKernelGGL(qmoe_route_grad<VV>, grid, block, lds, st, gw, logits, idx, idx64, T, E, k, over_all, b0, gl)
+    QMOE_BY_REGS(QMOE_CALL)
 #undef QMOE_CALL
-  return hipGetLastError();
+  });
 }
 
 hipError_t launch_sort_slots(const void* idx, bool idx64, int S, int E, int* hist, int* offsets, int* perm,
@@ -543,15 +570,16 @@ hipError_t launch_dispatch_rows(int type, const void* x, const int* inverse, int
   const long es = type == ROW_F32 ? 4 : 2;
   const bool wide = wide_ok(H * es, {x, rows});
   const long pieces = wide ? H * es / 16 : H;
-  int pl;
-  const dim3 grid = row_grid(T, pieces, &pl), block(256);
-  if (wide)
-    hipLaunchKernelGGL(qmoe_dispatch_rows<u32x4>, grid, block, 0, st, (const u32x4*)x, inverse, T, k, pieces, pl, (u32x4*)rows);
-  else if (es == 4)
-    hipLaunchKernelGGL(qmoe_dispatch_rows<uint32_t>, grid, block, 0, st, (const uint32_t*)x, inverse, T, k, pieces, pl, (uint32_t*)rows);
-  else
-    hipLaunchKernelGGL(qmoe_dispatch_rows<uint16_t>, grid, block, 0, st, (const uint16_t*)x, inverse, T, k, pieces, pl, (uint16_t*)rows);
-  return hipGetLastError();
+  const RowGrid r = row_grid(T, pieces);
+  return in_launches(r.x, [&](int b0, unsigned n) {
+    const dim3 grid(n, r.y), block(256);
+    if (wide)
+      hipLaunchKernelGGL(qmoe_dispatch_rows<u32x4>, grid, block, 0, st, (const u32x4*)x, inverse, T, k, pieces, r.per_log, b0, (u32x4*)rows);
+    else if (es == 4)
+      hipLaunchKernelGGL(qmoe_dispatch_rows<uint32_t>, grid, block, 0, st, (const uint32_t*)x, inverse, T, k, pieces, r.per_log, b0, (uint32_t*)rows);
+    else
+      hipLaunchKernelGGL(qmoe_dispatch_rows<uint16_t>, grid, block, 0, st, (const uint16_t*)x, inverse, T, k, pieces, r.per_log, b0, (uint16_t*)rows);
+  });
 }
 
 hipError_t launch_combine_rows(int type, const void* rows, const int* inverse, const float* w, int T, int k, long H,

@@ -1,0 +1,83 @@
+"""The steps of a routed layer at the ends of their documented ranges: more
+tokens and slots than one launch holds threads for."""
+import pytest
+
+import quantized_mixture_experts_router_amd as qm
+
+import steps_util as U
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def torch():
+    import torch as _t
+    if not _t.cuda.is_available():
+        pytest.skip("no GPU")
+    return _t
+
+
+def room(torch, gib):
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < gib << 30:
+        pytest.skip(f"needs {gib} GiB of GPU memory")
+
+
+@pytest.mark.parametrize("routing,normalize", [("qmoe", 0), ("moe", 0)])
+def test_route_of_2_to_the_26_tokens(torch, routing, normalize):
+    # 64 threads a token: 2^26 tokens are the 2^32 threads that one launch does not hold
+    room(torch, 16)
+    T = (1 << 26) + 5
+    U.say(f"[route] T={T} {routing}")
+    l = torch.randn(T, 2, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda")
+    a = {"k": 1, "routing": routing, "normalize_routing_weights": normalize}
+    idx, w = qm.route(l, a)
+    second = l[:, 1] > l[:, 0]  # equal logits: the lower expert
+    assert torch.equal(idx[:, 0] == 1, second)
+    d = (l[:, 0] - l[:, 1]).abs_()
+    ref = torch.ones_like(d) if routing == "qmoe" else 1 / (1 + torch.exp(-d))
+    assert float((w[:, 0] - ref).abs().max()) <= 16 * 2.0 ** -24
+    gl = qm.route_backward(torch.full((T, 1), 2.0, device="cuda"), l, idx, a)
+    if routing == "qmoe":  # the only expert of the selection: nothing to shift
+        assert not gl.any()
+    else:  # 2 p (1 - p), of opposite sign at the two experts
+        g = 2 * ref * (1 - ref)
+        g = torch.where(second, -g, g)
+        assert float((gl[:, 0] - g).abs().max()) <= 32 * 2.0 ** -24
+        assert float((gl[:, 1] + g).abs().max()) <= 32 * 2.0 ** -24
+
+
+def test_combine_backward_of_2_to_the_26_slots(torch):
+    # 64 threads a slot
+    room(torch, 16)
+    T, k = (1 << 25) + 3, 2
+    U.say(f"[combine grad] T={T} k={k}")
+    g = torch.Generator(device="cuda").manual_seed(2)
+    idx = torch.randint(-1, 3, (T, k), generator=g, device="cuda", dtype=torch.int32)
+    x = torch.randint(-8, 9, (T, 1), generator=g, device="cuda").float()  # products of small integers are exact
+    rows, off, perm, inv = qm.dispatch(x, idx, 3)
+    held = inv >= 0
+    n = int(held.sum())
+    assert off.tolist()[-1] == n
+    assert torch.equal(rows[:n, 0], x[perm[:n].long() // k, 0]) and not rows[n:].any()
+    w = torch.randint(1, 4, (T, k), generator=g, device="cuda").float()
+    gr, gw = qm.combine_backward(x, rows, inv, w)
+    assert torch.equal(gw, torch.where(held, x * x, 0.0))
+    assert torch.equal(gr[:n, 0], (w.view(-1)[perm[:n].long()] * rows[:n, 0])) and not gr[n:].any()
+    assert torch.equal(qm.combine(rows, inv, w), (w * held).sum(1, keepdim=True) * x)
+
+
+def test_dispatch_and_combine_of_2_to_the_24_long_rows(torch):
+    # 256 threads a token from 129 pieces a row on (129 bfloat16: one piece an element)
+    room(torch, 48)
+    T, H = (1 << 24) + 7, 129
+    U.say(f"[dispatch, combine] T={T} H={H}")
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randint(-100, 101, (T, H), generator=g, device="cuda", dtype=torch.int8).to(torch.bfloat16)
+    idx = torch.randint(0, 5, (T, 1), generator=g, device="cuda", dtype=torch.int32)
+    rows, off, perm, inv = qm.dispatch(x, idx, 5)
+    for i in range(0, T, 1 << 22):
+        assert torch.equal(rows[i:i + (1 << 22)], x[perm[i:i + (1 << 22)].long()]), i
+    out = qm.combine(rows, inv, torch.full((T, 1), 2.0, device="cuda"))
+    assert torch.equal(out, x + x)
+    assert torch.equal(qm.dispatch_backward(rows, inv), x)
