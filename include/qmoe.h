@@ -543,7 +543,8 @@ void qmoe_linear_attrs_default(qmoe_linear_attrs* a);
  * column, so a row's bits may differ between calls of other sizes or groups.
  * input and weights 16-byte aligned when K is a whole number of 16-byte runs
  * (else they are first copied to padded rows in the workspace).
- * G <= 1023, M <= 2^30, K and N <= 2^20 (QMOE_ERR_UNSUPPORTED).
+ * G <= 1023, M <= 2^30, K and N <= 2^20, and fewer than 2^31 tiles of 32 rows
+ * by 128 columns in any of the products (QMOE_ERR_UNSUPPORTED).
  * workspace: qmoe_linear_workspace_size bytes, 256-byte aligned (NULL when
  * 0). */
 qmoe_status qmoe_linear_workspace_size(const qmoe_tensor* input, const qmoe_tensor* weights, const qmoe_tensor* bias,

@@ -26,6 +26,7 @@
 #pragma once
 #include <type_traits>
 
+#include "launches.h"
 #include "linear_common.hpp"
 
 namespace qmoe {
@@ -190,7 +191,7 @@ struct LinOperand {
 };
 
 template <typename ET, int MODE, int BQ, int BP, int WQ, int WP, int NST, bool VEC, bool TURN>
-__global__ void __launch_bounds__(64 * WQ * WP) qmoe_linear(const LinearGemm g, int nq, int np) {
+__global__ void __launch_bounds__(64 * WQ * WP) qmoe_linear(const LinearGemm g, int nq, int np, int b0) {
   constexpr int NW = WQ * WP, TQ = BQ / WQ / 16, TP = BP / WP / 16;
   using OP = LinOperand<ET, BP, MODE == LIN_FWD, NW>;
   using OQ = LinOperand<ET, BQ, MODE != LIN_DW, NW>;
@@ -205,7 +206,7 @@ __global__ void __launch_bounds__(64 * WQ * WP) qmoe_linear(const LinearGemm g, 
   const RowBlocks blocks(MODE == LIN_DW ? nullptr : g.offsets, g.G, g.M, BQ);
   if (MODE != LIN_DW && g.offsets) nq = min(blocks.total, nq);
   if (nq <= 0) return;
-  const LinearTileAt tile = linear_tile_of(blockIdx.x, nq, np);
+  const LinearTileAt tile = linear_tile_of(b0 + blockIdx.x, nq, np);
   const int qb = tile.q, pb = tile.p;
   const int p0 = pb * BP;
   int grp, lo, hi, q0, qrows;  // group, its rows from the tile on, first output row, valid rows of the tile
@@ -476,20 +477,18 @@ hipError_t go_linear(const LinearGemm& g, bool vec, hipStream_t st) {
   const long qb = (rows + BQ - 1) / BQ;
   const long nq = MODE == LIN_DW ? qb * g.G : g.offsets ? qb + g.G + 1 : qb;
   const long np = (cols + BP - 1) / BP;
-  const dim3 grid((unsigned)linear_workgroups(nq, np), (unsigned)g.splits), block(64 * WQ * WP);
   auto go = [&](auto v, auto t) {
-    hipLaunchKernelGGL((qmoe_linear<ET, MODE, BQ, BP, WQ, WP, NST, decltype(v)::value, decltype(t)::value>), grid, block,
-                       0, st, g, (int)nq, (int)np);
+    return in_launches(linear_workgroups(nq, np), [&](int b0, unsigned n) {
+      const dim3 grid(n, (unsigned)g.splits), block(64 * WQ * WP);
+      hipLaunchKernelGGL((qmoe_linear<ET, MODE, BQ, BP, WQ, WP, NST, decltype(v)::value, decltype(t)::value>), grid,
+                         block, 0, st, g, (int)nq, (int)np, b0);
+    });
   };
-  auto turned = [&](auto t) { vec ? go(std::true_type{}, t) : go(std::false_type{}, t); };
+  auto turned = [&](auto t) { return vec ? go(std::true_type{}, t) : go(std::false_type{}, t); };
   if constexpr (MODE == LIN_FWD) {
-    if (g.offsets || nq == 1) {
-      turned(std::true_type{});
-      return hipGetLastError();
-    }
+    if (g.offsets || nq == 1) return turned(std::true_type{});
   }
-  turned(std::false_type{});
-  return hipGetLastError();
+  return turned(std::false_type{});
 }
 
 template <typename ET, int MODE>

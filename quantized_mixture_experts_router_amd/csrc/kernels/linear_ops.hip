@@ -3,6 +3,7 @@
 // sums, the bias gradient and row padding.  All are bound by HBM.
 #include <algorithm>
 
+#include "launches.h"
 #include "linear_common.hpp"
 
 namespace qmoe {
@@ -93,16 +94,16 @@ hipError_t finish_mode(int mode, const LinearGemm& g, hipStream_t st) {
 // time.  4096 x 14336 bfloat16, silu: 76 us for 352 MB, 4.6 TB/s of a copy's 4.9;
 // sums alone, 16384 x 4096: 35 us for 126 MB, 3.6 TB/s.
 template <typename ET, int ACT, bool VEC>
-__global__ void __launch_bounds__(256) qmoe_linear_act_grad(const LinearActGrad g, int ncol) {
+__global__ void __launch_bounds__(256) qmoe_linear_act_grad(const LinearActGrad g, int ncol, int b0) {
   constexpr int W = VEC ? 16 / (int)sizeof(ET) : 4, R = 4;
   constexpr bool glu = ACT == kActSwiglu;
   constexpr int H = glu ? W / 2 : W;
   __shared__ float red[3][64][W + 1];
-  const int rb = blockIdx.x / ncol;
+  const int b = b0 + (int)blockIdx.x, rb = b / ncol;
   int grp, lo, hi;
   if (!RowBlocks(g.offsets, g.G, g.M, kSumRows).find(rb, grp, lo, hi) || grp >= g.G) return;  // the whole workgroup
   const int lane = lane_id(), wave = threadIdx.x >> 6;
-  const int n = ((blockIdx.x % ncol) * 64 + lane) * W;
+  const int n = (b % ncol * 64 + lane) * W;
   const int left = g.N - n;  // columns from n on
   const long No = glu ? g.N >> 1 : g.N;
   const int m1 = min(hi, lo + kSumRows);
@@ -168,13 +169,14 @@ hipError_t go_act_grad(const LinearActGrad& g, hipStream_t st) {
   const long cols = g.dz && g.lddz > g.N ? g.lddz : g.N;
   const int per = 64 * (vec ? W : 4);
   const int ncol = (int)((cols + per - 1) / per);
-  const dim3 grid((unsigned)(blocks * ncol)), block(256);
-  with_act(g.act.type, [&](auto act) {
-    constexpr int A = decltype(act)::value;
-    if (vec) hipLaunchKernelGGL((qmoe_linear_act_grad<ET, A, true>), grid, block, 0, st, g, ncol);
-    else hipLaunchKernelGGL((qmoe_linear_act_grad<ET, A, false>), grid, block, 0, st, g, ncol);
+  return in_launches(blocks * ncol, [&](int b0, unsigned count) {
+    const dim3 grid(count), block(256);
+    with_act(g.act.type, [&](auto act) {
+      constexpr int A = decltype(act)::value;
+      if (vec) hipLaunchKernelGGL((qmoe_linear_act_grad<ET, A, true>), grid, block, 0, st, g, ncol, b0);
+      else hipLaunchKernelGGL((qmoe_linear_act_grad<ET, A, false>), grid, block, 0, st, g, ncol, b0);
+    });
   });
-  return hipGetLastError();
 }
 
 // One column a thread: the group's row blocks in order (14336 columns, 64

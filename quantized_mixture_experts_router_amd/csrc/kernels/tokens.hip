@@ -7,10 +7,10 @@
 // every output element has one writer, so results do not depend on order.
 #include <math.h>
 
-#include <algorithm>
 #include <type_traits>
 
 #include "common.hpp"
+#include "launches.h"
 #include "tokens.h"
 
 namespace qmoe {
@@ -457,20 +457,6 @@ bool wide_ok(long row_bytes, std::initializer_list<const void*> ps) {
   for (const void* p : ps)
     if (reinterpret_cast<uintptr_t>(p) & 15) return false;
   return true;
-}
-
-// One dimension of a launch holds fewer than 2^32 threads: `blocks` workgroups
-// of 256 in launches of 2^23 at most, f(first, count) each (2^26 tokens of the
-// router, 2^24 of long rows are the first that need two).
-constexpr long kMaxLaunch = 1l << 23;
-template <typename F>
-hipError_t in_launches(long blocks, F f) {
-  for (long b = 0; b < blocks; b += kMaxLaunch) {
-    f((int)b, (unsigned)std::min(blocks - b, kMaxLaunch));
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  return hipSuccess;
 }
 
 // Threads a token (log2) and the grid for rows of `pieces`: workgroups of

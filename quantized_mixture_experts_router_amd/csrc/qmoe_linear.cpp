@@ -150,7 +150,8 @@ qmoe_status check(const qmoe_tensor* input, const qmoe_tensor* weights, const qm
     if (t && (t->dims[0] != p->M || t->dims[1] != p->No)) return QMOE_ERR_SHAPE;
   if (p->G > kMaxGroups || p->M > kMaxRows || p->K > kMaxRow || p->N > kMaxRow) return QMOE_ERR_UNSUPPORTED;
   // one workgroup per tile and column block, tiles as small as 32 rows by 128
-  // columns; the passes one per 256 columns of 64 rows
+  // columns, the passes one per 256 columns of 64 rows: their indices (and
+  // nine q blocks more) stay within 32 bits
   const int64_t wide = std::max(p->N, p->K);
   if ((p->M / 32 + 9 + p->G) * (wide / 128 + 1) >= (int64_t(1) << 31) - 512 ||
       ((p->N / 32 + 1) * p->G + 8) * (p->K / 128 + 1) >= (int64_t(1) << 31) - 512)

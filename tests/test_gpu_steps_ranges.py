@@ -81,3 +81,29 @@ def test_dispatch_and_combine_of_2_to_the_24_long_rows(torch):
     out = qm.combine(rows, inv, torch.full((T, 1), 2.0, device="cuda"))
     assert torch.equal(out, x + x)
     assert torch.equal(qm.dispatch_backward(rows, inv), x)
+
+
+def test_linear_layer_of_2_to_the_30_rows(torch):
+    # the most rows there may be: 2^23 tiles of 128 rows, 2^24 row blocks of the bias gradient's sums at 256 threads each
+    room(torch, 120)
+    M, N = 1 << 30, 8
+    U.say(f"[linear] M={M}")
+    x = torch.zeros(M, N, dtype=torch.bfloat16, device="cuda")
+    dy = torch.zeros(M, N, dtype=torch.bfloat16, device="cuda")
+    at = torch.tensor([0, 1, 5000, (1 << 29) - 1, 1 << 29, (1 << 29) + 77, M - 129, M - 64, M - 1], device="cuda")
+    r = torch.arange(len(at) * N, device="cuda").view(-1, N)
+    x[at], dy[at] = (r % 7 - 3).bfloat16(), (r % 5 - 2).bfloat16()
+    w = (torch.arange(N * N, device="cuda").view(N, N) % 3 - 1).bfloat16()
+    y = qm.linear(x, w)
+    assert torch.equal(y[at], x[at] @ w.T)  # small integers: exact
+    y[at] = 0
+    for i in range(0, M, 1 << 28):
+        assert not y[i:i + (1 << 28)].any(), i
+    del y
+    gx, gw, gb = qm.linear_backward(dy, x, w, bias=True)
+    assert torch.equal(gx[at], dy[at] @ w)
+    assert torch.equal(gw, dy[at].T.contiguous() @ x[at])
+    assert torch.equal(gb, dy[at].float().sum(0).bfloat16())
+    gx[at] = 0
+    for i in range(0, M, 1 << 28):
+        assert not gx[i:i + (1 << 28)].any(), i
