@@ -30,10 +30,38 @@ __device__ __forceinline__ float lin_sigmoid(float v) {
   return 1.f / (1.f + expf(-v));
 }
 
+// The normal distribution Phi(z) and e = exp(-z^2 / 2).  Below 0 it is taken
+// as its own tail (1 + erf has lost 4 % of it at -5 and all of it at -5.6).
+// FAST: the tail is e times a polynomial in t = 1 / (1 + 0.3 |z|) (a fit of
+// Phi(-a) exp(a^2 / 2) over a in [0, 14], within 2^-22 relative), with the
+// hardware's exponential and reciprocal as above: 2^-20 in all, and z^2 2^-24
+// for the exponent's rounding, below 2^-9 of half a step of the 16-bit types.
+// Forward of 8192 x 1024 -> 4096 float16 84 us (105 us with erfcf, 93 us with
+// 1 + erff), the gradient's pass alone 42 us (70 and 52 us).
+struct LinPhi {
+  float phi, e;
+};
+template <bool FAST>
+__device__ __forceinline__ LinPhi lin_phi(float z) {
+  if constexpr (!FAST) return {0.5f * erfcf(z * -0.70710678118654752f), expf(-0.5f * z * z)};
+  const float e = __builtin_amdgcn_exp2f(z * z * -0.72134752044448170f);
+  const float t = __builtin_amdgcn_rcpf(fmaf(fabsf(z), 0.3f, 1.f));
+  float p = 0.03567499294877052f;
+  p = fmaf(p, t, -0.15720391273498535f);
+  p = fmaf(p, t, 0.20635481178760529f);
+  p = fmaf(p, t, -0.053684744983911514f);
+  p = fmaf(p, t, 0.12856215238571167f);
+  p = fmaf(p, t, 0.0999133437871933f);
+  p = fmaf(p, t, 0.12075397372245789f);
+  p = fmaf(p, t, 0.11962930113077164f);
+  const float tail = p * t * e;
+  return {z > 0.f ? 1.f - tail : tail, e};
+}
+
 template <bool FAST>
 __device__ __forceinline__ float lin_act(float z, int act) {
   if (act == kActRelu) return z < 0.f ? 0.f : z;  // NaN stays NaN
-  if (act == kActGelu) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+  if (act == kActGelu) return z * lin_phi<FAST>(z).phi;
   if (act == kActSilu) return z * lin_sigmoid<FAST>(z);
   return z;
 }
@@ -53,9 +81,8 @@ template <bool FAST>
 __device__ __forceinline__ float lin_act_grad(float dy, float z, int act) {
   if (act == kActRelu) return z > 0.f ? dy : 0.f;
   if (act == kActGelu) {
-    const float cdf = 0.5f * (1.f + erff(z * 0.70710678118654752f));
-    const float e = FAST ? __builtin_amdgcn_exp2f(z * z * -0.72134752044448170f) : expf(-0.5f * z * z);
-    return dy * (cdf + z * 0.39894228040143268f * e);
+    const LinPhi n = lin_phi<FAST>(z);
+    return dy * (n.phi + z * 0.39894228040143268f * n.e);
   }
   if (act == kActSilu) {
     const float s = lin_sigmoid<FAST>(z);
