@@ -103,7 +103,8 @@ __device__ __forceinline__ void lin_swiglu_grad(float dy, float g, float u, cons
     u = u > a.limit ? a.limit : u < -a.limit ? -a.limit : u;
   }
   const float s = lin_sigmoid<FAST>(a.alpha * g);
-  dg = gp ? dy * (u + a.beta) * s * (1.f + a.alpha * g * (1.f - s)) : 0.f;
+  // (alpha after g sigma (1 - sigma), which is small: alpha g alone may pass the largest float)
+  dg = gp ? dy * (u + a.beta) * (s + a.alpha * (g * s * (1.f - s))) : 0.f;
   du = up ? dy * g * s : 0.f;
 }
 

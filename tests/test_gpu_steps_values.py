@@ -1,5 +1,6 @@
 """Values at which the activations of the linear layers and their gradients
-lose digits: far negative arguments of GELU."""
+lose digits or leave the range: far negative arguments of GELU, and gates of
+any size the type holds."""
 import math
 
 import numpy as np
@@ -49,3 +50,42 @@ def test_gelu_far_below_zero(torch, dt):
     # (the gradient is rounded to the type as the operand of the product with 1, then the result: the same value)
     U.check(U.back(gx), gref, U.rounded(dt, gref, e), "gelu's gradient")
     U.check(U.back(gb), gref[0], U.rounded(dt, gref[0], e[0]), "bias gradient")
+
+
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("alpha,beta,limit", [(1.0, 0.0, None), (1.7, 0.5, None), (1.7, 1.0, 7.0)])
+def test_swiglu_gates_of_any_size(torch, dt, alpha, beta, limit):
+    # far below zero the gate shuts (output and gradients 0), far above it passes its value; no size of a finite gate
+    # makes a NaN
+    lowest = float(torch.finfo(getattr(torch, dt)).min)
+    gates = np.array([lowest, lowest / 2, -3e4, -200.0, -90.0, -30.0, 30.0, 200.0, 3e4, -lowest])
+    u = np.where(np.arange(10) % 2, -1.25, 1.25)
+    z = np.stack([gates, u], 1)
+    a = {"activation_type": "swiglu", "swiglu_fusion": 1, "activation_alpha": alpha, "activation_beta": beta,
+         "swiglu_limit": limit}
+    x, f = U.typed(torch, z, dt)
+    w = torch.eye(2, dtype=x.dtype, device="cuda")
+    y = qm.linear(x, w, attrs=a)
+    o = dict(alpha=alpha, beta=beta, limit=limit)
+    with np.errstate(over="ignore"):
+        ref, g = S.act(f, "swiglu", **o), S.act_grad(np.ones((10, 1)), f, "swiglu", **o)
+    # the gate's argument is rounded: sigma(v) of v with a relative error of 2^-22 is |v| 2^-22 off relative, and below
+    # e^-87 the float32 reciprocal gives 0
+    v = np.minimum(np.abs(alpha * f[:, :1]), 88.0)
+    rel = 2.0 ** -22 * (v + 16)
+    tiny = np.exp(-87.0) * (1 + np.minimum(np.abs(f[:, :1]), 4e4)) * 8
+    most = -lowest
+    got = U.back(y)
+    assert not np.isnan(got).any(), got
+    ok = np.abs(ref) < most  # beyond the type's range: infinite
+    U.check(np.where(ok, got, 0), np.where(ok, ref, 0), np.where(ok, U.rounded(dt, ref, rel * np.abs(ref) + tiny), 0),
+            "swiglu")
+    one = torch.ones(10, 1, dtype=x.dtype, device="cuda")
+    gx, _, _ = qm.linear_backward(one, x, w, x, None, a)
+    got = U.back(gx)
+    assert not np.isnan(got).any(), got
+    ok = np.abs(g) < most
+    # (1 + v) covers the term alpha g (1 - sigma) of the gate's gradient
+    e = rel * (1 + v) * np.abs(g) + tiny * (1 + v)
+    U.check(np.where(ok, got, 0), np.where(ok, g, 0), np.where(ok, U.rounded(dt, g, e) + U.HALF[dt] * np.abs(g), 0),
+            "swiglu's gradients")
