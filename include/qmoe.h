@@ -556,6 +556,14 @@ qmoe_status qmoe_linear(const qmoe_tensor* input, const qmoe_tensor* weights, co
                         const qmoe_tensor* output, const qmoe_tensor* preact, void* workspace, size_t workspace_bytes,
                         void* stream);
 
+/* How qmoe_linear and qmoe_linear_backward run the products of these shapes,
+ * as one line of text (validates first; pure host code): for each of forward=,
+ * grad_input= and grad_weights= the rows x columns of an output tile and,
+ * behind a colon, the ranges that the reduction is cut into.  At most len bytes
+ * are written to buf, NUL-terminated; NULL buf or len 0 is QMOE_ERR_NULL. */
+qmoe_status qmoe_linear_plan_describe(const qmoe_tensor* input, const qmoe_tensor* weights, const qmoe_tensor* offsets,
+                                      char* buf, size_t len);
+
 /* Gradients of qmoe_linear from grad_output [M, No] (which is also the
  * gradient at the residual):
  *

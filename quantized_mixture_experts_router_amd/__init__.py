@@ -13,7 +13,7 @@ and the current stream.  The functions keep the C names:
     qmoe_route, qmoe_route_backward, qmoe_dispatch_workspace_size,
     qmoe_dispatch, qmoe_dispatch_backward, qmoe_combine,
     qmoe_combine_backward, qmoe_linear_attrs_default,
-    qmoe_linear_workspace_size, qmoe_linear,
+    qmoe_linear_plan_describe, qmoe_linear_workspace_size, qmoe_linear,
     qmoe_linear_backward_workspace_size, qmoe_linear_backward
 
 plus ``forward``, ``grouped_matmul`` and ``moe_forward`` (allocate output and
@@ -150,6 +150,7 @@ def _lib():
                            ("qmoe_dispatch_backward", [D, D, D, P]),
                            ("qmoe_combine", [D, D, D, D, P]),
                            ("qmoe_combine_backward", [D] * 6 + [P]),
+                           ("qmoe_linear_plan_describe", [D, D, D, ctypes.c_char_p, Z]),
                            ("qmoe_linear_workspace_size", [D] * 5 + [LA, D, D, ZP]),
                            ("qmoe_linear", [D] * 5 + [LA, D, D, P, Z, P]),
                            ("qmoe_linear_backward_workspace_size", [D] * 5 + [LA, D, D, D, ZP]),
@@ -767,6 +768,14 @@ def _linear_a(attrs):
 
 def _refs(*ts):
     return [_ref(t, False) for t in ts]
+
+
+def qmoe_linear_plan_describe(input, weights, offsets=None) -> str:
+    """Tiles and ranges of the products of a linear layer and its gradients,
+    as one line of text.  Arrays may live anywhere."""
+    buf = ctypes.create_string_buffer(128)
+    _ok(_lib().qmoe_linear_plan_describe(*_refs(input, weights, offsets), buf, 128), "qmoe_linear_plan_describe")
+    return buf.value.decode()
 
 
 def qmoe_linear_workspace_size(input, weights, bias=None, residual=None, offsets=None, attrs=None, output=None,

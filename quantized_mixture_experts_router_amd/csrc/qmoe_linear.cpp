@@ -9,6 +9,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cstdio>
 
 #include "kernels/linear.h"
 #include "qmoe.h"
@@ -31,7 +32,7 @@ struct LinPlan {
   int type = LIN_F32;
   int64_t es = 4, Kp = 0, Np = 0;  // element size; K and N in whole 16-byte runs
   LinearAct act{};
-  LinearPlan fwd{}, dx{}, dw{};
+  LinearPlan fwd{LT_32x128, 1}, dx{LT_32x128, 1}, dw{LT_32x128, 1};
   size_t off_x = 0, off_w = 0, off_dz = 0, off_sums = 0, off_partial = 0;
   size_t bytes = 0;
 };
@@ -281,6 +282,29 @@ void qmoe_linear_attrs_default(qmoe_linear_attrs* a) {
   a->activation_beta = 0.f;
   a->has_swiglu_limit = 0;
   a->swiglu_limit = 0.f;
+}
+
+qmoe_status qmoe_linear_plan_describe(const qmoe_tensor* input, const qmoe_tensor* weights, const qmoe_tensor* offsets,
+                                      char* buf, size_t len) {
+  if (!buf || len == 0) return QMOE_ERR_NULL;
+  qmoe_linear_attrs a;
+  qmoe_linear_attrs_default(&a);
+  LinPlan p;
+  const qmoe_status st = check(input, weights, nullptr, offsets, nullptr, &a, {}, &p);
+  if (st != QMOE_OK) return st;
+  place_forward(&p);
+  place_backward(&p, true, true, true);
+  auto tile = [](const LinearPlan& pl) {
+    switch (pl.tile) {
+      case LT_256x256: return "256x256";
+      case LT_128x128: return "128x128";
+      case LT_64x128: return "64x128";
+    }
+    return "32x128";
+  };
+  std::snprintf(buf, len, "forward=%s:%d grad_input=%s:%d grad_weights=%s:%d", tile(p.fwd), p.fwd.splits, tile(p.dx),
+                p.dx.splits, tile(p.dw), p.dw.splits);
+  return QMOE_OK;
 }
 
 qmoe_status qmoe_linear_workspace_size(const qmoe_tensor* input, const qmoe_tensor* weights, const qmoe_tensor* bias,
