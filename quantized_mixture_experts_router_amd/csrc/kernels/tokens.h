@@ -19,9 +19,11 @@ hipError_t launch_route_grad(const float* gw, const float* logits, const void* i
                              bool over_all, float* gl, hipStream_t st);
 
 // Slots per block of the expert sort.  Up to kSortSelf slots every block
-// counts the experts of all slots itself (12288 slots: one launch of 24
-// blocks, against a counting launch and one block per 1024); beyond, a first
-// launch counts per block, with at most 256 blocks (each adds up the others').
+// counts the experts of all slots itself; beyond, a first launch counts per
+// block, with at most 256 blocks (each adds up the others').  One launch against
+// two, us: 4096 slots 4.6 / 7.4 (8 experts) and 5.0 / 8.8 (256), 12288 slots
+// 6.3 / 7.9 and 6.3 / 9.6, 16384 slots 7.1 / 7.6 and 6.9 / 8.7, 24576 slots
+// 8.9 / 8.1 and 8.2 / 9.2, 32768 slots 10.6 / 8.9 and 9.5 / 9.8.
 constexpr int kSortRound = 512;
 constexpr int kSortSelf = 16384;
 inline int sort_chunk(long S) {
