@@ -231,3 +231,34 @@ def test_large_tiles_of_element_aligned_tensors(torch, ints, dt, M, K, N, tiles)
     assert torch.equal(gx, product(torch, dy, w, None, False).to(t))
     assert torch.equal(gw, (dy.double().T @ x.double()).to(t))
     assert torch.equal(gb, dy.double().sum(0).to(t))
+
+
+@pytest.mark.parametrize("dt", ["float32", "bfloat16"])
+@pytest.mark.parametrize("G", [63, 64, 65, 127, 128, 129, 1023])
+def test_many_groups(torch, ints, dt, G):
+    # the walk over groups goes 64 at a time; the first offset is taken as 0
+    t = getattr(torch, dt)
+    r = np.random.default_rng(G)
+    counts = r.integers(0, 9, G) * (r.random(G) < 0.7)
+    counts[G - 1], counts[G // 2] = 70, 150
+    off = np.concatenate([[0], np.cumsum(counts)])
+    M, K, N = int(off[-1]) + 33, 72, 136
+    x, w, b, dy, z = ints(t, M, K), ints(t, G, N, K), ints(t, G, N), ints(t, M, N), ints(t, M, N)
+    first = int(off[1]) if off[1] else 0
+    given = off.copy()
+    given[0] = first // 2
+    d_off = torch.tensor(given, dtype=torch.int32, device="cuda")
+    U.say(f"[linear {dt}] {M} rows in {G} groups: {qm.qmoe_linear_plan_describe(x, w, d_off)}")
+    a = {"activation_type": "relu"}
+    y = qm.linear(x, w, b, None, d_off, a)
+    ref = product(torch, x, w, off, True)
+    for g, (lo, hi) in enumerate(spans(off, M)):
+        ref[lo:hi] += b[g].double()
+    assert torch.equal(y, ref.clamp(min=0).to(t))
+    gx, gw, gb = qm.linear_backward(dy, x, w, z, d_off, a, bias=True)
+    d = torch.where(z > 0, dy, torch.zeros_like(dy))
+    assert torch.equal(gx, product(torch, d, w, off, False).to(t))
+    for g, (lo, hi) in enumerate(spans(off, M)):
+        f = d[lo:hi].double()
+        assert torch.equal(gw[g], (f.T @ x[lo:hi].double()).to(t)), g
+        assert torch.equal(gb[g], f.sum(0).to(t)), g
