@@ -27,9 +27,9 @@ __device__ __forceinline__ int group_of_row(const int* __restrict__ offsets, int
 
 // Four columns of one output row a thread (two where rows allow no wide
 // access): the ranges' sums added in range order, then the epilogue (or the
-// store).  1001 x 1411 float32, two ranges, gelu, pre-activations kept: 7.2 us for
-// 23 MB (9.8 us with four columns a thread, whose single stores then lie 16 bytes
-// apart).
+// store).  1001 x 1411 float32, two ranges, gelu, pre-activations kept: 8.2 us for
+// 23 MB (four columns a thread, whose single stores then lie 16 bytes apart, took
+// 2.6 us more).
 template <typename ET, int MODE, bool VEC>
 __global__ void __launch_bounds__(256) qmoe_linear_finish(const LinearGemm g) {
   constexpr int W = VEC ? 4 : 2;
@@ -90,14 +90,15 @@ hipError_t finish_mode(int mode, const LinearGemm& g, hipStream_t st) {
 // dz of kSumRows rows of one group, W columns a lane (16 bytes where rows
 // allow it, VEC), and their column sums: float32, of the unrounded dz, in row
 // order (the four wavefronts take every fourth row each and add up in
-// wavefront order through LDS).  dz of the 16-bit types is rounded to the type:
-// it is the operand of two products on the 16-bit matrix instructions, nine
-// times as fast as the float32 ones that would take it unrounded.  The products
-// then carry two roundings of the same size, their operand's and their own: the
-// root mean square error of dx and dW is 0.00235 of the result's in bfloat16
-// (silu, 4096 x 4096 -> 14336), 0.00166 from unrounded dz.  Four rows of a
-// wavefront are in flight at a time.  4096 x 14336 bfloat16, silu: 76 us for 352 MB, 4.6 TB/s of a copy's 4.9;
-// sums alone, 16384 x 4096: 35 us for 126 MB, 3.6 TB/s.
+// wavefront order through LDS).  Four rows of a wavefront are in flight at a
+// time.  4096 x 14336 bfloat16, silu: 78 us for 352 MB, 4.5 TB/s of a copy's 4.9;
+// sums alone, 16384 x 4096: 36 us for 126 MB, 3.5 TB/s.
+// dz of the 16-bit types is rounded to the type: it is the operand of two
+// products on the 16-bit matrix instructions, nine times as fast as the float32
+// ones that would take it unrounded.  The products then carry two roundings of
+// the same size, their operand's and their own: the root mean square error of
+// dx and dW is 0.00235 of the result's in bfloat16 (silu, 4096 x 4096 -> 14336),
+// 0.00166 from unrounded dz.
 template <typename ET, int ACT, bool VEC>
 __global__ void __launch_bounds__(256) qmoe_linear_act_grad(const LinearActGrad g, int ncol, int b0) {
   constexpr int W = VEC ? 16 / (int)sizeof(ET) : 4, R = 4;

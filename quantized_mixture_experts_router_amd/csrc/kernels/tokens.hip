@@ -37,7 +37,7 @@ __device__ __forceinline__ int read_index(const void* idx, bool idx64, long i) {
 // One wavefront per token, logits e = lane + 64 j in registers.  A round takes
 // the largest value left (one wavefront maximum), then the lowest expert that
 // holds it (a ballot per register).  Bound by launch latency in decode (16 x 8
-// logits: 2.6 us).
+// logits: 2.5 us).
 template <int V>
 __global__ void __launch_bounds__(256) qmoe_route_topk(const float* __restrict__ logits, int T, int E, int k,
                                                        bool over_all, int b0, int* __restrict__ idx,
@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(256) qmoe_dispatch_rows(const U* __restrict__ 
 
 // A token's sum in registers, four of its rows in flight at a time, `per`
 // threads a token as above.  Bound by HBM: 65536 rows of 8 KB, half of them
-// dropped, to 8192 sums (278 MB to move) in 66 us, 4.2 TB/s.
+// dropped, to 8192 sums (278 MB to move) in 67 us, 4.1 TB/s.
 template <typename ET, bool WIDE>
 __global__ void __launch_bounds__(256) qmoe_combine_rows(const ET* __restrict__ rows, const int* __restrict__ inverse,
                                                          const float* __restrict__ w, int T, int k, long pieces,
@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(256) qmoe_combine_rows(const ET* __restrict__ 
 // A wavefront per slot (the slots of one token are neighbours and share its
 // gradient row in the caches): the row's product with its weight, and the dot
 // product, 64 pieces a step, added up across the wavefront at the end.  Bound by
-// HBM: 12282 rows of 4 KB read and written (109 MB) in 19.8 us, 5.5 TB/s.
+// HBM: 12282 rows of 4 KB read and written (109 MB) in 19.7 us, 5.5 TB/s.
 template <typename ET, bool WIDE>
 __global__ void __launch_bounds__(256) qmoe_combine_grad(const ET* __restrict__ gout, const ET* __restrict__ rows,
                                                          const int* __restrict__ inverse, const float* __restrict__ w,
