@@ -90,7 +90,8 @@ typedef enum {
   QMOE_I64 = 4,
   QMOE_F16 = 5,  /* GroupedMatMul, dispatch / combine and linear layers */
   QMOE_BF16 = 6, /* GroupedMatMul, dispatch / combine and linear layers */
-  QMOE_F64 = 7   /* GroupedMatMul only */
+  QMOE_F64 = 7,  /* GroupedMatMul only */
+  QMOE_E4M3 = 8  /* codes of rows held in 8 bits: 4 exponent and 3 mantissa bits, largest 448 */
 } qmoe_dtype;
 
 typedef enum {
@@ -589,6 +590,153 @@ qmoe_status qmoe_linear_backward(const qmoe_tensor* grad_output, const qmoe_tens
                                  const qmoe_linear_attrs* attrs, const qmoe_tensor* grad_input,
                                  const qmoe_tensor* grad_weights, const qmoe_tensor* grad_bias, void* workspace,
                                  size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * What stands in front of a routed layer and keeps its backward pass small:
+ * the root-mean-square norm with the residual's addition, routing from scores,
+ * and activations held in 8 bits from the forward to the backward pass.  A
+ * training step is qmoe_rms_norm (rows, and the same rows in 8 bits) ->
+ * qmoe_route_scored -> qmoe_dispatch -> qmoe_linear_q8 (FC1: its
+ * pre-activations in 8 bits) -> qmoe_linear (FC2) -> qmoe_combine; backward,
+ * qmoe_linear_backward_q8 reads both, and qmoe_route_scored_backward and
+ * qmoe_rms_norm_backward end it.  Types and conventions as for the steps above.
+ * ------------------------------------------------------------------------ */
+
+/* Rows in 8 bits: codes [M, N] and scales [M, ceil(N / block_size)] (float32),
+ * one scale per block_size columns of a row (16, 32, 64 or 128, else
+ * QMOE_ERR_ATTR; a row's last block may be shorter).  With m a block's largest
+ * magnitude its scale is 2^e, e the least integer from -126 on with
+ *   QMOE_U8    m <  127.5 2^e   code rint(v 2^-e) + 128 (1 .. 255)   value (code - 128) 2^e
+ *   QMOE_E4M3  m <= 464 2^e     code v 2^-e rounded to that type     value code 2^e
+ * and 1 for a block of zeros.  Both roundings are to nearest, ties to even; the
+ * value of a code is exact in every row type (one beyond the type's largest
+ * becomes that, float16's subnormal ones are rounded).  A block with a NaN or an
+ * infinity has the scale NaN: its codes are unspecified, its values NaN.
+ * input [M, N]: M <= 2^30, N <= 2^20 (QMOE_ERR_UNSUPPORTED). */
+qmoe_status qmoe_quantize_rows(const qmoe_tensor* input, int64_t block_size, const qmoe_tensor* codes,
+                               const qmoe_tensor* scales, void* stream);
+
+/* The values of rows in 8 bits: output [M, N], its rows those of codes [M, N];
+ * or, with perm [M] (int32, as qmoe_dispatch writes it for k slots a token) and
+ * codes [M / k, N], row m that of token perm[m] / k: the rows qmoe_dispatch made
+ * of tokens that are held once (zeros where perm lies outside [0, M)). */
+qmoe_status qmoe_dequantize_rows(const qmoe_tensor* codes, const qmoe_tensor* scales, int64_t block_size,
+                                 const qmoe_tensor* perm, const qmoe_tensor* output, void* stream);
+
+/* Root-mean-square norm of rows [M, H]:
+ *
+ *   sum    = input + residual              rounded to T; input without residual
+ *   output = sum weight / sqrt(mean over the row of sum^2 + epsilon)
+ *
+ * residual may be NULL (then sum must be, else QMOE_ERR_NULL); sum may be NULL;
+ * weight [H] NULL: 1.  The norm is of the rounded sum, so that it is the one of
+ * the tensor that the residual stream goes on with.  The result goes to output,
+ * rounded to T, and / or to codes and scales in 8 bits (codes and scales both or
+ * neither; from the float32 result; block_size is read with them).  epsilon > 0
+ * and finite (QMOE_ERR_ATTR).  Squares and their sum are float32: rows whose
+ * mean square passes its range give zeros; a NaN or an infinity spoils its own
+ * row.  M <= 2^30, H <= 2^20 (QMOE_ERR_UNSUPPORTED). */
+qmoe_status qmoe_rms_norm(const qmoe_tensor* input, const qmoe_tensor* residual, const qmoe_tensor* weight,
+                          float epsilon, const qmoe_tensor* sum, const qmoe_tensor* output, const qmoe_tensor* codes,
+                          const qmoe_tensor* scales, int64_t block_size, void* stream);
+
+/* Gradients of qmoe_rms_norm, input being its sum (its input where it had no
+ * residual).  With s = 1 / sqrt(mean(input^2) + epsilon), n = s input:
+ *
+ *   grad_input  = grad_sum + s (grad_output weight - n mean(grad_output weight n))
+ *   grad_weight = column sums of grad_output n
+ *
+ * grad_input [M, H] is the gradient at the forward's input and residual alike;
+ * grad_sum [M, H] is what arrives at sum itself (NULL: nothing).  Either result
+ * may be NULL; grad_weight needs weight (QMOE_ERR_NULL).  workspace:
+ * qmoe_rms_norm_backward_workspace_size bytes, 256-byte aligned (NULL when 0). */
+qmoe_status qmoe_rms_norm_backward_workspace_size(const qmoe_tensor* grad_output, const qmoe_tensor* grad_sum,
+                                                  const qmoe_tensor* input, const qmoe_tensor* weight, float epsilon,
+                                                  const qmoe_tensor* grad_input, const qmoe_tensor* grad_weight,
+                                                  size_t* bytes);
+qmoe_status qmoe_rms_norm_backward(const qmoe_tensor* grad_output, const qmoe_tensor* grad_sum,
+                                   const qmoe_tensor* input, const qmoe_tensor* weight, float epsilon,
+                                   const qmoe_tensor* grad_input, const qmoe_tensor* grad_weight, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
+typedef enum {
+  QMOE_SCORES_SOFTMAX = 0, /* softmax over all experts that are not masked */
+  QMOE_SCORES_SIGMOID = 1
+} qmoe_scores;
+
+/* Attributes of routing from scores, defaults in brackets. */
+typedef struct {
+  int32_t k;                         /* [1]  1 <= k <= kept_groups E / groups       */
+  int32_t scores;                    /* [SOFTMAX] qmoe_scores                       */
+  int32_t groups;                    /* [1]  equal groups of consecutive experts    */
+  int32_t kept_groups;               /* [1]  groups that experts are selected from  */
+  int32_t group_top;                 /* [2]  a group is ranked by its largest (1) or
+                                             the sum of its two largest (2)          */
+  int32_t normalize_routing_weights; /* [0]  1: weights divided by their sum        */
+  float scale;                       /* [1]  finite; multiplies the weights         */
+} qmoe_route_attrs;
+
+/* Fill *a with the defaults listed above.  a must not be NULL. */
+void qmoe_route_attrs_default(qmoe_route_attrs* a);
+
+/* Routing from scores: with s [T, E] the sigmoid of router_probs or their softmax,
+ * experts are ranked by s + bias (bias [E] float32, or NULL: 0), a balance
+ * correction that selects but does not weigh.  Of groups groups the kept_groups
+ * that rank highest (group_top) are kept, equal ones by ascending index; indices
+ * [T, k] (int32) = the k experts of those with the largest s + bias, largest first,
+ * equal ones by ascending index; weights [T, k] = scale times their s, divided by
+ * the sum of the k with normalize_routing_weights 1 (0 where that sum is 0).
+ * s counts as rounded to float32 (evaluated in 64 bits, rounded once; s + bias,
+ * group sums and weights float32), so the selection is exact.  A logit of
+ * -infinity or NaN masks its expert (no share in the softmax, never selected); a
+ * bias of -infinity or NaN keeps its expert from being selected.  A row with fewer
+ * than k experts left fills up with index -1 and weight 0.  A logit of +infinity
+ * counts as the largest float.  1 <= kept_groups <= groups, groups divides E
+ * (QMOE_ERR_ATTR); E <= 1024, groups <= 64, T * k < 2^30 (QMOE_ERR_UNSUPPORTED). */
+qmoe_status qmoe_route_scored(const qmoe_tensor* router_probs, const qmoe_tensor* bias, const qmoe_route_attrs* attrs,
+                              const qmoe_tensor* indices, const qmoe_tensor* weights, void* stream);
+
+/* Gradient of qmoe_route_scored at the logits: grad_router_probs [T, E] from
+ * grad_weights [T, k], with the forward's router_probs and indices (int32 or
+ * int64; attrs->k is not read).  The selection is constant, so the bias has no
+ * gradient.  Masked experts get 0, as do slots with an index outside [0, E). */
+qmoe_status qmoe_route_scored_backward(const qmoe_tensor* grad_weights, const qmoe_tensor* router_probs,
+                                       const qmoe_tensor* indices, const qmoe_route_attrs* attrs,
+                                       const qmoe_tensor* grad_router_probs, void* stream);
+
+/* qmoe_linear whose pre-activations leave in 8 bits for the backward pass: codes
+ * [M, N] and scales of the float32 pre-activations (before any rounding to T;
+ * rows behind the last group are zero).  Everything else as qmoe_linear. */
+qmoe_status qmoe_linear_q8_workspace_size(const qmoe_tensor* input, const qmoe_tensor* weights,
+                                          const qmoe_tensor* bias, const qmoe_tensor* residual,
+                                          const qmoe_tensor* offsets, const qmoe_linear_attrs* attrs,
+                                          const qmoe_tensor* output, const qmoe_tensor* codes,
+                                          const qmoe_tensor* scales, int64_t block_size, size_t* bytes);
+qmoe_status qmoe_linear_q8(const qmoe_tensor* input, const qmoe_tensor* weights, const qmoe_tensor* bias,
+                           const qmoe_tensor* residual, const qmoe_tensor* offsets, const qmoe_linear_attrs* attrs,
+                           const qmoe_tensor* output, const qmoe_tensor* codes, const qmoe_tensor* scales,
+                           int64_t block_size, void* workspace, size_t workspace_bytes, void* stream);
+
+/* qmoe_linear_backward with the input, the pre-activations or both held in 8
+ * bits: either is a tensor of T with its scales NULL, or codes with their scales
+ * (one block_size; each its own code type).  perm [M] (int32) or NULL: the input,
+ * held in 8 bits once a token ([M / k, K]), stands for the rows that
+ * qmoe_dequantize_rows makes of it; grad_input has all M rows.  Values that the
+ * codes stand for are exact in T, so the results are those of
+ * qmoe_linear_backward on the values (for float16 in its range).  Everything else
+ * as qmoe_linear_backward. */
+qmoe_status qmoe_linear_backward_q8_workspace_size(
+    const qmoe_tensor* grad_output, const qmoe_tensor* input, const qmoe_tensor* input_scales, const qmoe_tensor* perm,
+    const qmoe_tensor* weights, const qmoe_tensor* preact, const qmoe_tensor* preact_scales, int64_t block_size,
+    const qmoe_tensor* offsets, const qmoe_linear_attrs* attrs, const qmoe_tensor* grad_input,
+    const qmoe_tensor* grad_weights, const qmoe_tensor* grad_bias, size_t* bytes);
+qmoe_status qmoe_linear_backward_q8(const qmoe_tensor* grad_output, const qmoe_tensor* input,
+                                    const qmoe_tensor* input_scales, const qmoe_tensor* perm,
+                                    const qmoe_tensor* weights, const qmoe_tensor* preact,
+                                    const qmoe_tensor* preact_scales, int64_t block_size, const qmoe_tensor* offsets,
+                                    const qmoe_linear_attrs* attrs, const qmoe_tensor* grad_input,
+                                    const qmoe_tensor* grad_weights, const qmoe_tensor* grad_bias, void* workspace,
+                                    size_t workspace_bytes, void* stream);
 
 /* Static, human-readable name of a status code. */
 const char* qmoe_status_string(qmoe_status s);

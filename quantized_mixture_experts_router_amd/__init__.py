@@ -14,12 +14,19 @@ and the current stream.  The functions keep the C names:
     qmoe_dispatch, qmoe_dispatch_backward, qmoe_combine,
     qmoe_combine_backward, qmoe_linear_attrs_default,
     qmoe_linear_plan_describe, qmoe_linear_workspace_size, qmoe_linear,
-    qmoe_linear_backward_workspace_size, qmoe_linear_backward
+    qmoe_linear_backward_workspace_size, qmoe_linear_backward,
+    qmoe_quantize_rows, qmoe_dequantize_rows, qmoe_rms_norm,
+    qmoe_rms_norm_backward_workspace_size, qmoe_rms_norm_backward,
+    qmoe_route_attrs_default, qmoe_route_scored, qmoe_route_scored_backward,
+    qmoe_linear_q8_workspace_size, qmoe_linear_q8,
+    qmoe_linear_backward_q8_workspace_size, qmoe_linear_backward_q8
 
 plus ``forward``, ``grouped_matmul`` and ``moe_forward`` (allocate output and
 workspace with torch, then call the entry point) for convenience, and the
 same for the steps of a routed layer and their gradients: ``route``,
-``dispatch``, ``combine``, ``linear`` and their ``*_backward``.  The
+``dispatch``, ``combine``, ``linear`` and their ``*_backward``, and for what
+stands around them: ``rms_norm``, ``route_scored``, ``quantize_rows``,
+``dequantize_rows``, ``linear_q8``, ``linear_backward_q8``.  The
 library is loaded on first use; a missing build raises immediately, there is
 no fallback.
 """
@@ -36,9 +43,10 @@ from typing import Optional
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libqmoe.so")
 
-QMOE_F32, QMOE_U8, QMOE_I32, QMOE_I64, QMOE_F16, QMOE_BF16, QMOE_F64 = 1, 2, 3, 4, 5, 6, 7
+QMOE_F32, QMOE_U8, QMOE_I32, QMOE_I64, QMOE_F16, QMOE_BF16, QMOE_F64, QMOE_E4M3 = 1, 2, 3, 4, 5, 6, 7, 8
 QMOE_ACT = {"relu": 0, "swiglu": 1, "gelu": 2, "silu": 3, "identity": 4}
 QMOE_ROUTING = {"qmoe": 0, "moe": 1}
+QMOE_SCORES = {"softmax": 0, "sigmoid": 1}
 STATUS = {0: "OK", 1: "NULL", 2: "SHAPE", 3: "ATTR", 4: "UNSUPPORTED", 5: "WORKSPACE", 6: "HIP",
           7: "DTYPE", 8: "ALIGN"}
 
@@ -69,6 +77,12 @@ class QmoeLinearAttrs(ctypes.Structure):
     _fields_ = [("activation_type", ctypes.c_int32), ("swiglu_fusion", ctypes.c_int32),
                 ("activation_alpha", ctypes.c_float), ("activation_beta", ctypes.c_float),
                 ("has_swiglu_limit", ctypes.c_int32), ("swiglu_limit", ctypes.c_float)]
+
+
+class QmoeRouteAttrs(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_int32), ("scores", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("kept_groups", ctypes.c_int32), ("group_top", ctypes.c_int32),
+                ("normalize_routing_weights", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
 QMOE_STAGE_EVENTS = 6
@@ -141,7 +155,7 @@ def _lib():
         lib.qmoe_moe_forward_debug.restype = ctypes.c_int
         LA, I32, I64, P, Z = (ctypes.POINTER(QmoeLinearAttrs), ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p,
                               ctypes.c_size_t)
-        ZP = ctypes.POINTER(ctypes.c_size_t)
+        ZP, RA, F = ctypes.POINTER(ctypes.c_size_t), ctypes.POINTER(QmoeRouteAttrs), ctypes.c_float
         D = P  # tensors as addresses into the packed arguments (_pack)
         for name, args in (("qmoe_route", [D, I32, I32, I32, D, D, P]),
                            ("qmoe_route_backward", [D, D, D, I32, I32, D, P]),
@@ -154,11 +168,24 @@ def _lib():
                            ("qmoe_linear_workspace_size", [D] * 5 + [LA, D, D, ZP]),
                            ("qmoe_linear", [D] * 5 + [LA, D, D, P, Z, P]),
                            ("qmoe_linear_backward_workspace_size", [D] * 5 + [LA, D, D, D, ZP]),
-                           ("qmoe_linear_backward", [D] * 5 + [LA, D, D, D, P, Z, P])):
+                           ("qmoe_linear_backward", [D] * 5 + [LA, D, D, D, P, Z, P]),
+                           ("qmoe_quantize_rows", [D, I64, D, D, P]),
+                           ("qmoe_dequantize_rows", [D, D, I64, D, D, P]),
+                           ("qmoe_rms_norm", [D, D, D, F, D, D, D, D, I64, P]),
+                           ("qmoe_rms_norm_backward_workspace_size", [D, D, D, D, F, D, D, ZP]),
+                           ("qmoe_rms_norm_backward", [D, D, D, D, F, D, D, P, Z, P]),
+                           ("qmoe_route_scored", [D, D, RA, D, D, P]),
+                           ("qmoe_route_scored_backward", [D, D, D, RA, D, P]),
+                           ("qmoe_linear_q8_workspace_size", [D] * 5 + [LA, D, D, D, I64, ZP]),
+                           ("qmoe_linear_q8", [D] * 5 + [LA, D, D, D, I64, P, Z, P]),
+                           ("qmoe_linear_backward_q8_workspace_size", [D] * 7 + [I64, D, LA, D, D, D, ZP]),
+                           ("qmoe_linear_backward_q8", [D] * 7 + [I64, D, LA, D, D, D, P, Z, P])):
             getattr(lib, name).argtypes = args
             getattr(lib, name).restype = ctypes.c_int
         lib.qmoe_linear_attrs_default.argtypes = [LA]
         lib.qmoe_linear_attrs_default.restype = None
+        lib.qmoe_route_attrs_default.argtypes = [RA]
+        lib.qmoe_route_attrs_default.restype = None
         lib.qmoe_status_string.argtypes = [ctypes.c_int]
         lib.qmoe_status_string.restype = ctypes.c_char_p
         _lib_handle = lib
@@ -176,7 +203,7 @@ def describe(t, data: bool = True) -> QmoeTensor:
     shape = tuple(t.shape)  # ranks above 3 pass through so the library rejects them
     name = str(t.dtype).replace("torch.", "")
     code = {"float32": QMOE_F32, "uint8": QMOE_U8, "int32": QMOE_I32, "int64": QMOE_I64, "float16": QMOE_F16,
-            "bfloat16": QMOE_BF16, "float64": QMOE_F64}.get(name, 0)
+            "bfloat16": QMOE_BF16, "float64": QMOE_F64, "float8_e4m3fn": QMOE_E4M3}.get(name, 0)
     ptr = None
     if data and hasattr(t, "data_ptr"):
         if not t.is_contiguous():
@@ -484,7 +511,7 @@ def moe_forward(tensors: dict, attrs=None, stream=None, workspace=None, output=N
 # library reads during the call only.
 _ONE = struct.Struct("=qiiqqq").pack_into
 _CODES = {"float32": QMOE_F32, "uint8": QMOE_U8, "int32": QMOE_I32, "int64": QMOE_I64, "float16": QMOE_F16,
-          "bfloat16": QMOE_BF16, "float64": QMOE_F64}
+          "bfloat16": QMOE_BF16, "float64": QMOE_F64, "float8_e4m3fn": QMOE_E4M3}
 _code_of = {}  # torch dtype -> code, filled as types are met
 _tls = threading.local()
 
@@ -498,7 +525,7 @@ def _pack(ts, first=0):
     buffer from place ``first`` on, valid until its next _pack of that place."""
     buf = getattr(_tls, "buf", None)
     if buf is None:
-        buf = _tls.buf = ctypes.create_string_buffer(40 * 12)
+        buf = _tls.buf = ctypes.create_string_buffer(40 * 16)
         _tls.at = ctypes.addressof(buf)
     at, off, out = _tls.at, 40 * first, []
     for t in ts:
@@ -858,4 +885,292 @@ def linear_backward(grad_output, input, weights, preact=None, offsets=None, attr
             "qmoe_linear_backward_workspace_size")
         w, n, _keep = _ws(workspace, need.value, input)
         _ok(lib.qmoe_linear_backward(*t[:5], attr, *t[5:], w, n, st), "qmoe_linear_backward")
+    return gi, gw, gb
+
+
+# ------------------------------------------------------------------ rows in 8 bits
+def _code_type(format):
+    """torch type of the codes of "int8" (uint8, 128 for 0) or "e4m3"."""
+    import torch
+    if format == "int8":
+        return torch.uint8
+    if format == "e4m3":
+        return torch.float8_e4m3fn
+    raise ValueError(f"no 8-bit format {format!r} (int8 or e4m3)")
+
+
+def _eight(like, format, rows, cols, block_size):
+    """Empty codes and scales of rows x cols values."""
+    import torch
+    blocks = -(-cols // block_size) if block_size > 0 else 0  # (the library refuses other sizes)
+    return like.new_empty((rows, cols), dtype=_code_type(format)), like.new_empty((rows, blocks), dtype=torch.float32)
+
+
+def qmoe_quantize_rows(input, block_size, codes, scales, stream=None) -> None:
+    """Enqueue rows to 8 bits: codes [M, N] uint8 or float8_e4m3fn, scales
+    [M, ceil(N / block_size)] float32."""
+    ctx, st = _on(stream, (input, codes, scales))
+    with ctx:
+        x, c, s = _pack((input, codes, scales))
+        _ok(_lib().qmoe_quantize_rows(x, block_size, c, s, st), "qmoe_quantize_rows")
+
+
+def quantize_rows(input, format="int8", block_size=128, stream=None):
+    """Allocate and qmoe_quantize_rows: (codes, scales); format "int8" or "e4m3"."""
+    ctx, st = _on(stream, (input,))
+    with ctx:
+        codes, scales = _eight(input, format, input.shape[0], input.shape[-1], block_size)
+        x, c, s = _pack((input, codes, scales))
+        _ok(_lib().qmoe_quantize_rows(x, block_size, c, s, st), "qmoe_quantize_rows")
+    return codes, scales
+
+
+def qmoe_dequantize_rows(codes, scales, block_size, perm, output, stream=None) -> None:
+    """Enqueue the values of rows in 8 bits; perm None: row for row."""
+    ctx, st = _on(stream, (codes, scales, perm, output))
+    with ctx:
+        c, s, p, o = _pack((codes, scales, perm, output))
+        _ok(_lib().qmoe_dequantize_rows(c, s, block_size, p, o, st), "qmoe_dequantize_rows")
+
+
+def dequantize_rows(codes, scales, dtype, block_size=128, perm=None, stream=None, output=None):
+    """Allocate output of ``dtype`` unless given, then qmoe_dequantize_rows:
+    the rows of codes, or with ``perm`` (of qmoe_dispatch) the slots' rows."""
+    ctx, st = _on(stream, (codes, scales, perm, output))
+    with ctx:
+        if output is None:
+            rows = codes.shape[0] if perm is None else perm.shape[0]
+            output = codes.new_empty((rows, codes.shape[1]), dtype=dtype)
+        c, s, p, o = _pack((codes, scales, perm, output))
+        _ok(_lib().qmoe_dequantize_rows(c, s, block_size, p, o, st), "qmoe_dequantize_rows")
+    return output
+
+
+# ------------------------------------------------------------------ norm
+def qmoe_rms_norm(input, residual, weight, epsilon, sum, output, codes=None, scales=None, block_size=128,
+                  stream=None) -> None:
+    """Enqueue the root-mean-square norm; residual, weight, sum, output, or
+    codes and scales may be None (not output and codes both)."""
+    ctx, st = _on(stream, (input, residual, weight, sum, output, codes, scales))
+    with ctx:
+        x, r, w, h, y, c, s = _pack((input, residual, weight, sum, output, codes, scales))
+        _ok(_lib().qmoe_rms_norm(x, r, w, epsilon, h, y, c, s, block_size, st), "qmoe_rms_norm")
+
+
+def rms_norm(input, weight=None, residual=None, epsilon=1e-6, format=None, block_size=128, keep_output=True,
+             stream=None):
+    """Allocate and qmoe_rms_norm: (output, sum, codes, scales), sum None
+    without residual, codes and scales None without ``format`` ("int8" or
+    "e4m3"), output None unless ``keep_output``."""
+    import torch
+    ctx, st = _on(stream, (input, weight, residual))
+    with ctx:
+        output = torch.empty_like(input) if keep_output else None
+        sum = torch.empty_like(input) if residual is not None else None
+        codes = scales = None
+        if format is not None:
+            codes, scales = _eight(input, format, input.shape[0], input.shape[-1], block_size)
+        x, r, w, h, y, c, s = _pack((input, residual, weight, sum, output, codes, scales))
+        _ok(_lib().qmoe_rms_norm(x, r, w, epsilon, h, y, c, s, block_size, st), "qmoe_rms_norm")
+    return output, sum, codes, scales
+
+
+def qmoe_rms_norm_backward_workspace_size(grad_output, grad_sum, input, weight, epsilon=1e-6, grad_input=None,
+                                          grad_weight=None) -> int:
+    """Workspace bytes of qmoe_rms_norm_backward for the gradients given.  Arrays may live anywhere."""
+    n = ctypes.c_size_t(0)
+    _ok(_lib().qmoe_rms_norm_backward_workspace_size(*_refs(grad_output, grad_sum, input, weight), epsilon,
+                                                     *_refs(grad_input, grad_weight), ctypes.byref(n)),
+        "qmoe_rms_norm_backward_workspace_size")
+    return n.value
+
+
+def qmoe_rms_norm_backward(grad_output, grad_sum, input, weight, epsilon, grad_input, grad_weight, workspace=None,
+                           stream=None) -> None:
+    """Enqueue the gradients of qmoe_rms_norm (either may be None); input is the
+    forward's sum, or its input where it had no residual."""
+    ctx, st = _on(stream, (grad_output, grad_sum, input, weight, grad_input, grad_weight, workspace))
+    with ctx:
+        w, n, _keep = _ws(workspace, 0, input)
+        t = _pack((grad_output, grad_sum, input, weight, grad_input, grad_weight))
+        _ok(_lib().qmoe_rms_norm_backward(*t[:4], epsilon, *t[4:], w, n, st), "qmoe_rms_norm_backward")
+
+
+def rms_norm_backward(grad_output, input, weight=None, grad_sum=None, epsilon=1e-6, stream=None, workspace=None):
+    """Allocate and qmoe_rms_norm_backward: (grad_input, grad_weight),
+    grad_weight None without weight."""
+    import torch
+    ctx, st = _on(stream, (grad_output, input, weight, grad_sum, workspace))
+    with ctx:
+        gi = torch.empty_like(input)
+        gw = torch.empty_like(weight) if weight is not None else None
+        lib, need = _lib(), ctypes.c_size_t(0)
+        t = _pack((grad_output, grad_sum, input, weight, gi, gw))
+        _ok(lib.qmoe_rms_norm_backward_workspace_size(*t[:4], epsilon, *t[4:], ctypes.byref(need)),
+            "qmoe_rms_norm_backward_workspace_size")
+        w, n, _keep = _ws(workspace, need.value, input)
+        _ok(lib.qmoe_rms_norm_backward(*t[:4], epsilon, *t[4:], w, n, st), "qmoe_rms_norm_backward")
+    return gi, gw
+
+
+# ------------------------------------------------------------------ routing from scores
+_ROUTE_ATTRS = frozenset(f[0] for f in QmoeRouteAttrs._fields_)
+
+
+def qmoe_route_attrs_default() -> QmoeRouteAttrs:
+    a = QmoeRouteAttrs()
+    _lib().qmoe_route_attrs_default(ctypes.byref(a))
+    return a
+
+
+def make_route_attrs(attrs: Optional[dict] = None) -> QmoeRouteAttrs:
+    """qmoe_route_attrs from a dict of its fields ("scores" also by name)."""
+    a = QmoeRouteAttrs(1, QMOE_SCORES["softmax"], 1, 1, 2, 0, 1.0)  # qmoe_route_attrs_default
+    for key, val in (attrs or {}).items():
+        if key not in _ROUTE_ATTRS:
+            raise ValueError(f"no attribute {key!r} of routing from scores")
+        if key == "scores" and isinstance(val, str):
+            val = QMOE_SCORES.get(val, 99)
+        setattr(a, key, val)
+    return a
+
+
+def _scored_a(attrs):
+    return attrs if isinstance(attrs, QmoeRouteAttrs) else make_route_attrs(attrs)
+
+
+def qmoe_route_scored(router_probs, bias, attrs, indices, weights, stream=None) -> None:
+    """Enqueue routing from scores; bias may be None, indices int32 and weights
+    float32 are [T, k]."""
+    route_scored(router_probs, bias, attrs, stream, indices, weights)
+
+
+def route_scored(router_probs, bias=None, attrs=None, stream=None, indices=None, weights=None):
+    """Allocate what is not given, then qmoe_route_scored: (indices, weights)."""
+    import torch
+    a = _scored_a(attrs)
+    ctx, st = _on(stream, (router_probs, bias, indices, weights))
+    with ctx:
+        if indices is None:
+            indices = router_probs.new_empty((router_probs.shape[0], max(a.k, 0)), dtype=torch.int32)
+        if weights is None:
+            weights = router_probs.new_empty(indices.shape, dtype=torch.float32)
+        p, b, i, w = _pack((router_probs, bias, indices, weights))
+        _ok(_lib().qmoe_route_scored(p, b, ctypes.byref(a), i, w, st), "qmoe_route_scored")
+    return indices, weights
+
+
+def qmoe_route_scored_backward(grad_weights, router_probs, indices, attrs, grad_router_probs, stream=None) -> None:
+    """Enqueue the gradient of qmoe_route_scored at the logits (k is indices'
+    second extent)."""
+    route_scored_backward(grad_weights, router_probs, indices, attrs, stream, grad_router_probs)
+
+
+def route_scored_backward(grad_weights, router_probs, indices, attrs=None, stream=None, grad_router_probs=None):
+    """Allocate grad_router_probs [T, E] unless given, then qmoe_route_scored_backward."""
+    import torch
+    a = _scored_a(attrs)
+    ctx, st = _on(stream, (grad_weights, router_probs, indices, grad_router_probs))
+    with ctx:
+        if grad_router_probs is None:
+            grad_router_probs = torch.empty_like(router_probs)
+        g, p, i, o = _pack((grad_weights, router_probs, indices, grad_router_probs))
+        _ok(_lib().qmoe_route_scored_backward(g, p, i, ctypes.byref(a), o, st), "qmoe_route_scored_backward")
+    return grad_router_probs
+
+
+# ------------------------------------------------------------------ linear layers and their checkpoints
+def _pair(t):
+    """(tensor, None), or (codes, scales) of what is held in 8 bits."""
+    return t if isinstance(t, (tuple, list)) else (t, None)
+
+
+def qmoe_linear_q8_workspace_size(input, weights, bias=None, residual=None, offsets=None, attrs=None, output=None,
+                                  codes=None, scales=None, block_size=128) -> int:
+    """Workspace bytes of qmoe_linear_q8.  Arrays may live anywhere."""
+    a, n = _linear_a(attrs), ctypes.c_size_t(0)
+    _ok(_lib().qmoe_linear_q8_workspace_size(*_refs(input, weights, bias, residual, offsets), ctypes.byref(a),
+                                             *_refs(output, codes, scales), block_size, ctypes.byref(n)),
+        "qmoe_linear_q8_workspace_size")
+    return n.value
+
+
+def qmoe_linear_q8(input, weights, bias, residual, offsets, attrs, output, codes, scales, block_size=128,
+                   workspace=None, stream=None) -> None:
+    """Enqueue a linear layer whose pre-activations [M, N] leave in 8 bits; the
+    rest as qmoe_linear."""
+    a = _linear_a(attrs)
+    ctx, st = _on(stream, (input, weights, bias, residual, offsets, output, codes, scales, workspace))
+    with ctx:
+        w, n, _keep = _ws(workspace, 0, input)
+        t = _pack((input, weights, bias, residual, offsets, output, codes, scales))
+        _ok(_lib().qmoe_linear_q8(*t[:5], ctypes.byref(a), *t[5:], block_size, w, n, st), "qmoe_linear_q8")
+
+
+def linear_q8(input, weights, bias=None, residual=None, offsets=None, attrs=None, format="int8", block_size=128,
+              stream=None, workspace=None, output=None):
+    """Allocate and qmoe_linear_q8: (output, codes, scales)."""
+    a = _linear_a(attrs)
+    ctx, st = _on(stream, (input, weights, bias, residual, offsets, workspace, output))
+    with ctx:
+        M, N = input.shape[0], weights.shape[-2]
+        if output is None:
+            output = input.new_empty((M, N // 2 if a.activation_type == QMOE_ACT["swiglu"] else N))
+        codes, scales = _eight(input, format, M, N, block_size)
+        lib, need, attr = _lib(), ctypes.c_size_t(0), ctypes.byref(a)
+        t = _pack((input, weights, bias, residual, offsets, output, codes, scales))
+        _ok(lib.qmoe_linear_q8_workspace_size(*t[:5], attr, *t[5:], block_size, ctypes.byref(need)),
+            "qmoe_linear_q8_workspace_size")
+        w, n, _keep = _ws(workspace, need.value, input)
+        _ok(lib.qmoe_linear_q8(*t[:5], attr, *t[5:], block_size, w, n, st), "qmoe_linear_q8")
+    return output, codes, scales
+
+
+def qmoe_linear_backward_q8_workspace_size(grad_output, input, weights, preact=None, offsets=None, attrs=None,
+                                           grad_input=None, grad_weights=None, grad_bias=None, block_size=128,
+                                           perm=None) -> int:
+    """Workspace bytes of qmoe_linear_backward_q8 for the gradients given; input
+    and preact tensors or (codes, scales).  Arrays may live anywhere."""
+    a, n = _linear_a(attrs), ctypes.c_size_t(0)
+    (x, xs), (z, zs) = _pair(input), _pair(preact)
+    _ok(_lib().qmoe_linear_backward_q8_workspace_size(
+        *_refs(grad_output, x, xs, perm, weights, z, zs), block_size, *_refs(offsets), ctypes.byref(a),
+        *_refs(grad_input, grad_weights, grad_bias), ctypes.byref(n)), "qmoe_linear_backward_q8_workspace_size")
+    return n.value
+
+
+def qmoe_linear_backward_q8(grad_output, input, weights, preact, offsets, attrs, grad_input, grad_weights, grad_bias,
+                            block_size=128, perm=None, workspace=None, stream=None) -> None:
+    """Enqueue the gradients of qmoe_linear from an input and pre-activations
+    that are each a tensor or (codes, scales); with ``perm`` the input's codes
+    are held once a token.  The rest as qmoe_linear_backward."""
+    a = _linear_a(attrs)
+    (x, xs), (z, zs) = _pair(input), _pair(preact)
+    ctx, st = _on(stream, (grad_output, x, xs, perm, weights, z, zs, offsets, grad_input, grad_weights, grad_bias,
+                           workspace))
+    with ctx:
+        w, n, _keep = _ws(workspace, 0, weights)
+        t = _pack((grad_output, x, xs, perm, weights, z, zs, offsets, grad_input, grad_weights, grad_bias))
+        _ok(_lib().qmoe_linear_backward_q8(*t[:7], block_size, t[7], ctypes.byref(a), *t[8:], w, n, st),
+            "qmoe_linear_backward_q8")
+
+
+def linear_backward_q8(grad_output, input, weights, preact=None, offsets=None, attrs=None, bias=False, block_size=128,
+                       perm=None, stream=None, workspace=None):
+    """Allocate and qmoe_linear_backward_q8: (grad_input, grad_weights,
+    grad_bias), grad_bias None unless ``bias``."""
+    import torch
+    a = _linear_a(attrs)
+    (x, xs), (z, zs) = _pair(input), _pair(preact)
+    ctx, st = _on(stream, (grad_output, x, xs, perm, weights, z, zs, offsets, workspace))
+    with ctx:
+        gi = weights.new_empty((grad_output.shape[0], weights.shape[-1]))
+        gw = torch.empty_like(weights)
+        gb = weights.new_empty(weights.shape[:-1]) if bias else None
+        lib, need, attr = _lib(), ctypes.c_size_t(0), ctypes.byref(a)
+        t = _pack((grad_output, x, xs, perm, weights, z, zs, offsets, gi, gw, gb))
+        _ok(lib.qmoe_linear_backward_q8_workspace_size(*t[:7], block_size, t[7], attr, *t[8:], ctypes.byref(need)),
+            "qmoe_linear_backward_q8_workspace_size")
+        w, n, _keep = _ws(workspace, need.value, weights)
+        _ok(lib.qmoe_linear_backward_q8(*t[:7], block_size, t[7], attr, *t[8:], w, n, st), "qmoe_linear_backward_q8")
     return gi, gw, gb

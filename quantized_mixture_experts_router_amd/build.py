@@ -23,6 +23,9 @@ SOURCES = [
     "qmoe_moe.cpp",
     "qmoe_tokens.cpp",
     "qmoe_linear.cpp",
+    "qmoe_rows8.cpp",
+    "qmoe_norm.cpp",
+    "qmoe_route_scored.cpp",
     "kernels/route.hip",
     "kernels/operand.hip",
     "kernels/gemm.hip",
@@ -33,6 +36,9 @@ SOURCES = [
     "kernels/gmm_typed.hip",
     "kernels/moe.hip",
     "kernels/tokens.hip",
+    "kernels/rows8.hip",
+    "kernels/norm.hip",
+    "kernels/route_scored.hip",
     "kernels/linear_ops.hip",
     "kernels/linear_f16.hip",
     "kernels/linear_bf16.hip",

@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "rows8.h"
+
 namespace qmoe {
 
 enum LinearType { LIN_F32 = 0, LIN_F16 = 1, LIN_BF16 = 2 };
@@ -32,6 +34,7 @@ struct LinearGemm {
   const void* bias;  // [G][N] or NULL   (LIN_FWD)
   const void* res;   // [M][ldo] or NULL (LIN_FWD)
   void* pre;         // [M][N] or NULL   (LIN_FWD)
+  Rows8 pre8;        // in 8 bits; codes NULL: not (LIN_FWD)
   void* out;         // [M][No], dx [M][K] or dw [G][N][K]
   float* partial;    // splits > 1: [splits][rows of out][cols4] fp32 sums
   int splits;        // ranges of r
@@ -51,13 +54,14 @@ hipError_t launch_linear_finish(int type, int mode, const LinearGemm& g, hipStre
 // dz = dy * act'(z) (rows of the groups only) into dz [M][lddz], columns from
 // N on zeroed, and the column sums of each row block into sums (kSumRows rows
 // of a group each, [blocks][N]); dz or sums may be NULL.  z is NULL for the
-// identity.
+// identity or where z8 holds it.
 constexpr int kSumRows = 64;
 // Row blocks of M rows in G groups (G < 0: no groups), at most.
 constexpr long linear_sum_blocks(long M, long G) { return (M + kSumRows - 1) / kSumRows + (G < 0 ? 0 : G + 1); }
 struct LinearActGrad {
   const void* dy;  // [M][No]
-  const void* z;   // [M][N]
+  const void* z;   // [M][N], or NULL
+  Rows8 z8;        // the same in 8 bits; codes NULL: not
   void* dz;
   long lddz;
   float* sums;

@@ -8,6 +8,7 @@
 #include "common.hpp"
 #include "linear.h"
 #include "linear_tiles.h"
+#include "rows8.hpp"
 
 namespace qmoe {
 
@@ -302,6 +303,42 @@ __device__ __forceinline__ void linear_rows(const LinearGemm& g, float (&z)[R][W
     for (int r = 0; r < R; ++r)
       if (ok[r]) store_w<ET, W, VEC>(out + (long)m[r] * g.N, n, z[r]);
   }
+}
+
+// Pre-activations z + b of W consecutive columns c .. of R output rows in 8 bits:
+// the lanes of one block of columns are neighbours, and every one of them is
+// here (columns from N on hold zeros).
+template <int W, int R>
+__device__ __forceinline__ void linear_rows8(const LinearGemm& g, const float (&z)[R][W], const float (&b)[W], int c,
+                                             const int (&m)[R], const bool (&ok)[R]) {
+  const int n = g.N - c, bl = g.pre8.block_log;
+  const int blocks = (g.N + (1 << bl) - 1) >> bl;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    float v[W];
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      v[i] = z[r][i] + b[i];
+      top = max(top, abs_bits(v[i]));
+    }
+    top = lanes_max(top, bl - (W == 4 ? 2 : 1));
+    const uint32_t s = g.pre8.format == R8_INT8 ? r8_scale_bits<R8_INT8>(top) : r8_scale_bits<R8_E4M3>(top);
+    if (!ok[r] || n <= 0) continue;
+    uint8_t* p = g.pre8.codes + (long)m[r] * g.N + c;
+    if (g.pre8.format == R8_INT8) store_codes<R8_INT8, W>(p, n, v, r8_inverse(s));
+    else store_codes<R8_E4M3, W>(p, n, v, r8_inverse(s));
+    if ((c & ((1 << bl) - 1)) == 0) g.pre8.scales[(long)m[r] * blocks + (c >> bl)] = __uint_as_float(s);
+  }
+}
+
+// Zeros in 8 bits in the four columns from n on of row m.
+__device__ __forceinline__ void linear_zero8(const Rows8& q, int N, int m, int n) {
+  const int bl = q.block_log;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (n + i < N) q.codes[(long)m * N + n + i] = q.format == R8_INT8 ? 128 : 0;
+  if (n < N && (n & ((1 << bl) - 1)) == 0) q.scales[(long)m * ((N + (1 << bl) - 1) >> bl) + (n >> bl)] = 1.f;
 }
 
 // f(ACT) with the activation as a compile-time constant.

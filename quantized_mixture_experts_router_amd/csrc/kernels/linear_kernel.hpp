@@ -190,7 +190,8 @@ struct LinOperand {
   }
 };
 
-template <typename ET, int MODE, int BQ, int BP, int WQ, int WP, int NST, bool VEC, bool TURN>
+// Q8: the pre-activations leave in 8 bits (LIN_FWD).
+template <typename ET, int MODE, int BQ, int BP, int WQ, int WP, int NST, bool VEC, bool TURN, bool Q8>
 __global__ void __launch_bounds__(64 * WQ * WP) qmoe_linear(const LinearGemm g, int nq, int np, int b0) {
   constexpr int NW = WQ * WP, TQ = BQ / WQ / 16, TP = BP / WP / 16;
   using OP = LinOperand<ET, BP, MODE == LIN_FWD, NW>;
@@ -232,6 +233,7 @@ __global__ void __launch_bounds__(64 * WQ * WP) qmoe_linear(const LinearGemm g, 
       for (int i = threadIdx.x; i < min(qrows, BQ) * (BP / 4); i += 64 * NW) {
         const int m = q0 + i / (BP / 4), c = p0 + 4 * (i % (BP / 4));
         linear_zero<ET, MODE>(g, m, c);
+        if constexpr (Q8) linear_zero8(g.pre8, g.N, m, c);
       }
       return;
     }
@@ -439,7 +441,7 @@ __global__ void __launch_bounds__(64 * WQ * WP) qmoe_linear(const LinearGemm g, 
       }
       continue;
     }
-    if (!inside) continue;
+    if (!Q8 && !inside) continue;
     auto rows = [&](auto act) QMOE_INLINE {
       for (int s0 = 0; s0 < WQ * 32; s0 += RPS * RS) {
         float z[RS][W];
@@ -456,6 +458,10 @@ __global__ void __launch_bounds__(64 * WQ * WP) qmoe_linear(const LinearGemm g, 
           for (int i = 0; i < W; ++i) z[r][i] = v[i];
         }
         if constexpr (MODE == LIN_FWD) {
+          if constexpr (Q8) {
+            linear_rows8<W, RS>(g, z, bias, c, m, ok);
+            if (!inside) continue;
+          }
           linear_rows<ET, decltype(act)::value, W, RS, VEC>(g, z, bias, c, m, ok);
         } else {
           ET* out = static_cast<ET*>(g.out) + (MODE == LIN_DW ? (long)grp * g.N * g.K : 0) + c;
@@ -477,12 +483,18 @@ hipError_t go_linear(const LinearGemm& g, bool vec, hipStream_t st) {
   const long qb = (rows + BQ - 1) / BQ;
   const long nq = MODE == LIN_DW ? qb * g.G : g.offsets ? qb + g.G + 1 : qb;
   const long np = (cols + BP - 1) / BP;
-  auto go = [&](auto v, auto t) {
+  auto go8 = [&](auto v, auto t, auto q) {
     return in_launches(linear_workgroups(nq, np), [&](int b0, unsigned n) {
       const dim3 grid(n, (unsigned)g.splits), block(64 * WQ * WP);
-      hipLaunchKernelGGL((qmoe_linear<ET, MODE, BQ, BP, WQ, WP, NST, decltype(v)::value, decltype(t)::value>), grid,
+      hipLaunchKernelGGL((qmoe_linear<ET, MODE, BQ, BP, WQ, WP, NST, decltype(v)::value, decltype(t)::value, decltype(q)::value>), grid,
                          block, 0, st, g, (int)nq, (int)np, b0);
     });
+  };
+  auto go = [&](auto v, auto t) {
+    if constexpr (MODE == LIN_FWD) {
+      if (g.pre8.codes) return go8(v, t, std::true_type{});
+    }
+    return go8(v, t, std::false_type{});
   };
   auto turned = [&](auto t) { return vec ? go(std::true_type{}, t) : go(std::false_type{}, t); };
   if constexpr (MODE == LIN_FWD) {

@@ -68,6 +68,53 @@ __global__ void __launch_bounds__(256) qmoe_linear_finish(const LinearGemm g) {
   } else if (c < g.K) store_w<ET, W, VEC>(static_cast<ET*>(g.out) + row * g.K + c, g.K - c, z[0]);
 }
 
+// The same for a forward product whose pre-activations leave in 8 bits: a row's
+// threads are whole blocks of columns, so that a block's lanes are neighbours.
+template <typename ET, bool VEC>
+__global__ void __launch_bounds__(256) qmoe_linear_finish8(const LinearGemm g, int b0) {
+  constexpr int W = VEC ? 4 : 2;
+  typedef float V __attribute__((ext_vector_type(W)));
+  const int bl = g.pre8.block_log;
+  const long ldp = (g.N + 3) & ~3, per = (((long)g.N + (1 << bl) - 1) >> bl << bl) / W;
+  const long i = (long)(b0 + blockIdx.x) * 256 + threadIdx.x, row = i / per;
+  const int c = (int)(i - row * per) * W;
+  if (row >= g.M) return;
+  const int grp = group_of_row(g.offsets, g.G, g.M, (int)row);
+  if (grp >= g.G) {
+    if (c % 4 != 0) return;
+    linear_zero<ET, LIN_FWD>(g, (int)row, c);
+    linear_zero8(g.pre8, g.N, (int)row, c);
+    return;
+  }
+  float z[1][W] = {};
+  if (c < ldp) {
+#pragma unroll 4
+    for (int s = 0; s < g.splits; ++s) {
+      const V v = *(const V*)(g.partial + ((long)s * g.M + row) * ldp + c);
+#pragma unroll
+      for (int j = 0; j < W; ++j) z[0][j] += v[j];
+    }
+  }
+  float b[W] = {};
+  const int m[1] = {(int)row};
+  const bool ok[1] = {true};
+  if (g.bias && c < g.N) load_w<ET, W, VEC>(static_cast<const ET*>(g.bias) + (long)grp * g.N + c, g.N - c, b);
+  linear_rows8<W, 1>(g, z, b, c, m, ok);
+  if (c >= g.N) return;
+  with_act(g.act.type, [&](auto act) { linear_rows<ET, decltype(act)::value, W, 1, VEC>(g, z, b, c, m, ok); });
+}
+
+template <typename ET>
+hipError_t go_finish8(const LinearGemm& g, hipStream_t st) {
+  const bool vec = linear_vec<ET>(g, LIN_FWD);
+  const long block = 1l << g.pre8.block_log;
+  const long n = (long)g.M * ((g.N + block - 1) / block * block / (vec ? 4 : 2));
+  return in_launches((n + 255) / 256, [&](int b0, unsigned count) {
+    if (vec) hipLaunchKernelGGL((qmoe_linear_finish8<ET, true>), dim3(count), dim3(256), 0, st, g, b0);
+    else hipLaunchKernelGGL((qmoe_linear_finish8<ET, false>), dim3(count), dim3(256), 0, st, g, b0);
+  });
+}
+
 template <typename ET, int MODE>
 hipError_t go_finish(const LinearGemm& g, hipStream_t st) {
   const long cols = MODE == LIN_FWD ? g.N : g.K;
@@ -82,7 +129,7 @@ hipError_t go_finish(const LinearGemm& g, hipStream_t st) {
 
 template <typename ET>
 hipError_t finish_mode(int mode, const LinearGemm& g, hipStream_t st) {
-  if (mode == LIN_FWD) return go_finish<ET, LIN_FWD>(g, st);
+  if (mode == LIN_FWD) return g.pre8.codes ? go_finish8<ET>(g, st) : go_finish<ET, LIN_FWD>(g, st);
   if (mode == LIN_DX) return go_finish<ET, LIN_DX>(g, st);
   return go_finish<ET, LIN_DW>(g, st);
 }
@@ -99,7 +146,8 @@ hipError_t finish_mode(int mode, const LinearGemm& g, hipStream_t st) {
 // the same size, their operand's and their own: the root mean square error of
 // dx and dW is 0.00235 of the result's in bfloat16 (silu, 4096 x 4096 -> 14336),
 // 0.00166 from unrounded dz.
-template <typename ET, int ACT, bool VEC>
+// Z8: the format of z where that is held in 8 bits, else -1.
+template <typename ET, int ACT, bool VEC, int Z8>
 __global__ void __launch_bounds__(256) qmoe_linear_act_grad(const LinearActGrad g, int ncol, int b0) {
   constexpr int W = VEC ? 16 / (int)sizeof(ET) : 4, R = 4;
   constexpr bool glu = ACT == kActSwiglu;
@@ -128,7 +176,13 @@ __global__ void __launch_bounds__(256) qmoe_linear_act_grad(const LinearActGrad 
       for (int i = 0; i < W; ++i) z[r][i] = 0.f;
       if (ok) {
         load_w<ET, H, VEC>(dyp + row * No, glu ? left >> 1 : left, dy[r]);
-        if constexpr (ACT != kActIdentity) load_w<ET, W, VEC>(zp + row * g.N, left, z[r]);
+        if constexpr (ACT != kActIdentity) {
+          if constexpr (Z8 >= 0) {
+            const int bl = g.z8.block_log;
+            const float s = g.z8.scales[row * ((g.N + (1 << bl) - 1) >> bl) + (n >> bl)];
+            load_codes<ET, Z8, W>(g.z8.codes + row * g.N + n, left, s, z[r]);
+          } else load_w<ET, W, VEC>(zp + row * g.N, left, z[r]);
+        }
       }
     }
 #pragma unroll
@@ -179,8 +233,15 @@ hipError_t go_act_grad(const LinearActGrad& g, hipStream_t st) {
     const dim3 grid(count), block(256);
     with_act(g.act.type, [&](auto act) {
       constexpr int A = decltype(act)::value;
-      if (vec) hipLaunchKernelGGL((qmoe_linear_act_grad<ET, A, true>), grid, block, 0, st, g, ncol, b0);
-      else hipLaunchKernelGGL((qmoe_linear_act_grad<ET, A, false>), grid, block, 0, st, g, ncol, b0);
+      auto go = [&](auto z8) {
+        constexpr int Z = decltype(z8)::value;
+        if (vec) hipLaunchKernelGGL((qmoe_linear_act_grad<ET, A, true, Z>), grid, block, 0, st, g, ncol, b0);
+        else hipLaunchKernelGGL((qmoe_linear_act_grad<ET, A, false, Z>), grid, block, 0, st, g, ncol, b0);
+      };
+      if constexpr (A != kActIdentity) {
+        if (g.z8.codes) return with_format(g.z8.format, go);
+      }
+      go(std::integral_constant<int, -1>{});
     });
   });
 }

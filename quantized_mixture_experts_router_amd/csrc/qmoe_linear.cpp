@@ -3,7 +3,7 @@
 //
 // Forward:  [row padding] -> matrix kernel (epilogue inside, or fp32 sums per
 //           range of K -> finishing pass)
-// Backward: [row padding] -> activation gradient with column sums -> bias
+// Backward: [row padding, 8-bit input to rows] -> activation gradient with column sums -> bias
 //           gradient -> grad_input product -> grad_weights product
 // with every intermediate in the caller's workspace.
 #include <hip/hip_runtime.h>
@@ -12,13 +12,11 @@
 #include <cstdio>
 
 #include "kernels/linear.h"
-#include "qmoe.h"
+#include "qmoe_checks.h"
 
 using namespace qmoe;
 
 namespace {
-
-bool aligned_to(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
@@ -33,6 +31,7 @@ struct LinPlan {
   int64_t es = 4, Kp = 0, Np = 0;  // element size; K and N in whole 16-byte runs
   LinearAct act{};
   LinearPlan fwd{LT_32x128, 1}, dx{LT_32x128, 1}, dw{LT_32x128, 1};
+  bool x8 = false;  // backward: the input is held in 8 bits
   size_t off_x = 0, off_w = 0, off_dz = 0, off_sums = 0, off_partial = 0;
   size_t bytes = 0;
 };
@@ -89,12 +88,6 @@ LinearPlan plan_product(int type, int64_t rows, int64_t groups, int64_t cols, in
     }
   }
   return best;
-}
-
-int64_t numel(const qmoe_tensor* t) {
-  int64_t n = 1;
-  for (int i = 0; i < t->rank; ++i) n *= t->dims[i];
-  return n;
 }
 
 qmoe_status check_act(const qmoe_linear_attrs* a, LinearAct* act) {
@@ -193,8 +186,8 @@ bool needs_dz(const LinPlan& p) { return p.act.type != QMOE_ACT_IDENTITY || p.Np
 void place_backward(LinPlan* p, bool gx, bool gw, bool gb) {
   size_t o = 0;
   auto take = [&](size_t bytes) { size_t at = o; o = align256(o + bytes); return at; };
+  if (gw && (p->Kp != p->K || p->x8)) p->off_x = take((size_t)(p->M * p->Kp * p->es));
   if (p->Kp != p->K) {
-    if (gw) p->off_x = take((size_t)(p->M * p->Kp * p->es));
     if (gx) p->off_w = take((size_t)(wrows(*p) * p->Kp * p->es));
   }
   if ((gx || gw) && needs_dz(*p)) p->off_dz = take((size_t)(p->M * p->Np * p->es));
@@ -236,25 +229,6 @@ qmoe_status check_grads(const qmoe_tensor* grad_output, const qmoe_tensor* input
   return QMOE_OK;
 }
 
-// Pointers present where there are elements, and aligned: operands of the
-// matrix kernel to 16 bytes when their rows are whole 16-byte runs (they are
-// copied to such rows otherwise), everything else to the element.
-qmoe_status check_data(std::initializer_list<const qmoe_tensor*> ts, int64_t es) {
-  for (const qmoe_tensor* t : ts) {
-    if (!t) continue;
-    if (numel(t) > 0 && !t->data) return QMOE_ERR_NULL;
-    if (!aligned_to(t->data, (uintptr_t)es)) return QMOE_ERR_ALIGN;
-  }
-  return QMOE_OK;
-}
-
-qmoe_status check_ws(const void* ws, size_t have, size_t need) {
-  if (need == 0) return QMOE_OK;
-  if (!ws) return QMOE_ERR_NULL;
-  if (have < need) return QMOE_ERR_WORKSPACE;
-  return aligned_to(ws, 256) ? QMOE_OK : QMOE_ERR_ALIGN;
-}
-
 // One product: matrix kernel, and the finishing pass when it ran in ranges.
 bool run_product(int type, int mode, const LinearPlan& pl, LinearGemm g, float* partial, hipStream_t s) {
   g.splits = pl.splits;
@@ -277,6 +251,159 @@ LinearGemm base_gemm(const LinPlan& p, const qmoe_tensor* input, const qmoe_tens
   g.K = (int)p.K;
   g.act = p.act;
   return g;
+}
+
+// qmoe_linear, and with codes and scales qmoe_linear_q8.
+qmoe_status forward(const qmoe_tensor* input, const qmoe_tensor* weights, const qmoe_tensor* bias,
+                    const qmoe_tensor* residual, const qmoe_tensor* offsets, const qmoe_linear_attrs* attrs,
+                    const qmoe_tensor* output, const qmoe_tensor* preact, const qmoe_tensor* codes,
+                    const qmoe_tensor* scales, int64_t block_size, void* workspace, size_t workspace_bytes,
+                    void* stream) {
+  if (!output) return QMOE_ERR_NULL;
+  LinPlan p;
+  qmoe_status st = check(input, weights, bias, offsets, preact, attrs, {residual, output}, &p);
+  if (st == QMOE_OK && codes) st = check_rows8(codes, scales, p.M, p.N, block_size);
+  if (st != QMOE_OK) return st;
+  if (p.M == 0 || p.N == 0) return QMOE_OK;
+  place_forward(&p);
+  const uintptr_t op = p.Kp == p.K ? 16 : (uintptr_t)p.es;
+  st = check_data({input, weights, bias, residual, offsets, output, preact, codes, scales});
+  if (st != QMOE_OK) return st;
+  // operands of the matrix kernel to 16 bytes where their rows are whole 16-byte runs (they are copied to such rows otherwise)
+  if (!aligned_to(input->data, op) || !aligned_to(weights->data, op)) return QMOE_ERR_ALIGN;
+  st = check_ws(workspace, workspace_bytes, p.bytes);
+  if (st != QMOE_OK) return st;
+
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  LinearGemm g = base_gemm(p, input, weights, offsets);
+  g.bias = bias ? bias->data : nullptr;
+  g.res = residual ? residual->data : nullptr;
+  g.out = const_cast<void*>(output->data);
+  g.pre = preact ? const_cast<void*>(preact->data) : nullptr;
+  if (codes) g.pre8 = rows8_of(codes, scales, block_size);
+  if (p.Kp != p.K) {
+    if (launch_linear_pad((int)p.es, {g.x, p.M, p.K, ws + p.off_x, p.Kp}, {g.w, wrows(p), p.K, ws + p.off_w, p.Kp}, s) !=
+        hipSuccess)
+      return QMOE_ERR_HIP;
+    g.x = ws + p.off_x;
+    g.w = ws + p.off_w;
+    g.ldx = g.ldw = p.Kp;
+  }
+  return run_product(p.type, LIN_FWD, p.fwd, g, reinterpret_cast<float*>(ws + p.off_partial), s) ? QMOE_OK
+                                                                                                : QMOE_ERR_HIP;
+}
+
+// What qmoe_linear_backward_q8 has beside qmoe_linear_backward: scales of an input
+// or pre-activations held in 8 bits, and the input's rows.
+struct Held {
+  const qmoe_tensor *input_scales, *preact_scales, *perm;
+  int64_t block_size;
+};
+
+// The contract of qmoe_linear_backward_q8: what is held in 8 bits is checked as
+// such, and stands as a tensor of the weights' type in the checks that both share.
+qmoe_status check_held(const qmoe_tensor* grad_output, const qmoe_tensor* input, const qmoe_tensor* weights,
+                       const qmoe_tensor* preact, const qmoe_tensor* offsets, const qmoe_linear_attrs* attrs,
+                       const qmoe_tensor* grad_input, const qmoe_tensor* grad_weights, const qmoe_tensor* grad_bias,
+                       const Held& h, LinPlan* p) {
+  if (!grad_output || !input || !weights) return QMOE_ERR_NULL;
+  if (grad_output->rank != 2 || input->rank != 2 || (preact && preact->rank != 2) || (h.perm && h.perm->rank != 1))
+    return QMOE_ERR_SHAPE;
+  if (!float_code(weights->dtype)) return QMOE_ERR_DTYPE;
+  const bool x8 = eight_code(input->dtype), z8 = preact && eight_code(preact->dtype);
+  if ((x8 && !h.input_scales) || (z8 && !h.preact_scales)) return QMOE_ERR_NULL;
+  if ((!x8 && (h.input_scales || h.perm)) || (!z8 && h.preact_scales)) return QMOE_ERR_DTYPE;
+  if (h.perm && h.perm->dtype != QMOE_I32) return QMOE_ERR_DTYPE;
+  const int64_t M = grad_output->dims[0], T = input->dims[0];
+  if (T < 0 || M < 0) return QMOE_ERR_SHAPE;
+  if (h.perm ? h.perm->dims[0] != M || (T == 0 ? M != 0 : M % T != 0) : T != M) return QMOE_ERR_SHAPE;
+  qmoe_tensor x = *input, z{};
+  x.dims[0] = M;
+  if (x8) x.dtype = weights->dtype;
+  if (preact) {
+    z = *preact;
+    if (z8) z.dtype = weights->dtype;
+  }
+  qmoe_status st = check(&x, weights, grad_bias, offsets, preact ? &z : nullptr, attrs, {grad_output}, p);
+  if (st == QMOE_OK && x8) st = check_rows8(input, h.input_scales, T, p->K, h.block_size);
+  if (st == QMOE_OK && z8) st = check_rows8(preact, h.preact_scales, p->M, p->N, h.block_size);
+  if (st != QMOE_OK) return st;
+  p->x8 = x8;
+  return check_grads(grad_output, &x, weights, preact ? &z : nullptr, offsets, attrs, grad_input, grad_weights, grad_bias, p);
+}
+
+// Enqueues the gradients of a checked call.
+qmoe_status backward(const LinPlan& p, const qmoe_tensor* grad_output, const qmoe_tensor* input,
+                     const qmoe_tensor* weights, const qmoe_tensor* preact, const qmoe_tensor* offsets,
+                     const qmoe_tensor* grad_input, const qmoe_tensor* grad_weights, const qmoe_tensor* grad_bias,
+                     const Held& h, void* workspace, size_t workspace_bytes, void* stream) {
+  qmoe_status st = check_data({grad_output, input, h.input_scales, h.perm, weights, preact, h.preact_scales, offsets, grad_input, grad_weights, grad_bias});
+  if (st != QMOE_OK) return st;
+  const uintptr_t op = p.Kp == p.K ? 16 : (uintptr_t)p.es;
+  if ((!p.x8 && !aligned_to(input->data, op)) || !aligned_to(weights->data, op)) return QMOE_ERR_ALIGN;
+  if (!needs_dz(p) && !aligned_to(grad_output->data, 16)) return QMOE_ERR_ALIGN;
+  st = check_ws(workspace, workspace_bytes, p.bytes);
+  if (st != QMOE_OK) return st;
+
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const bool gx = grad_input && p.M > 0 && p.K > 0;
+  const bool gw = grad_weights && p.G > 0 && p.N > 0 && p.K > 0;
+  const bool gb = grad_bias && p.G > 0 && p.N > 0;
+  LinearGemm g = base_gemm(p, input, weights, offsets);
+  g.dz = grad_output->data;
+  float* sums = gb ? reinterpret_cast<float*>(ws + p.off_sums) : nullptr;
+  const bool dz = (gx || gw) && needs_dz(p);
+  if (p.M > 0 && p.N > 0 && (dz || gb)) {
+    LinearActGrad a{};
+    a.dy = grad_output->data;
+    if (p.act.type != QMOE_ACT_IDENTITY) {
+      if (h.preact_scales) a.z8 = rows8_of(preact, h.preact_scales, h.block_size);
+      else a.z = preact->data;
+    }
+    a.dz = dz ? ws + p.off_dz : nullptr;
+    a.lddz = p.Np;
+    a.sums = sums;
+    a.offsets = g.offsets;
+    a.G = g.G;
+    a.M = g.M;
+    a.N = g.N;
+    a.act = p.act;
+    if (launch_linear_act_grad(p.type, a, s) != hipSuccess) return QMOE_ERR_HIP;
+    if (dz) {
+      g.dz = ws + p.off_dz;
+      g.lddz = p.Np;
+    }
+  }
+  if (gb && launch_linear_bias_grad(p.type, sums, g.offsets, g.G, g.M, g.N, const_cast<void*>(grad_bias->data), s) !=
+                hipSuccess)
+    return QMOE_ERR_HIP;
+  float* partial = reinterpret_cast<float*>(ws + p.off_partial);
+  if (p.x8 && gw && p.M > 0) {
+    if (launch_dequantize_rows(row_type(weights->dtype), rows8_of(input, h.input_scales, h.block_size),
+                               h.perm ? static_cast<const int*>(h.perm->data) : nullptr,
+                               (int)(p.M / input->dims[0]), p.M, p.K, ws + p.off_x, p.Kp, s) != hipSuccess)
+      return QMOE_ERR_HIP;
+    g.x = ws + p.off_x;
+  }
+  if (p.Kp != p.K) {
+    if (launch_linear_pad((int)p.es, {g.x, gw && !p.x8 ? p.M : 0, p.K, ws + p.off_x, p.Kp},
+                          {g.w, gx ? wrows(p) : 0, p.K, ws + p.off_w, p.Kp}, s) != hipSuccess)
+      return QMOE_ERR_HIP;
+    g.x = ws + p.off_x;
+    g.w = ws + p.off_w;
+    g.ldx = g.ldw = p.Kp;
+  }
+  if (gx) {
+    g.out = const_cast<void*>(grad_input->data);
+    if (!run_product(p.type, LIN_DX, p.dx, g, partial, s)) return QMOE_ERR_HIP;
+  }
+  if (gw) {
+    g.out = const_cast<void*>(grad_weights->data);
+    if (!run_product(p.type, LIN_DW, p.dw, g, partial, s)) return QMOE_ERR_HIP;
+  }
+  return QMOE_OK;
 }
 
 }  // namespace
@@ -332,37 +459,32 @@ qmoe_status qmoe_linear(const qmoe_tensor* input, const qmoe_tensor* weights, co
                         const qmoe_tensor* residual, const qmoe_tensor* offsets, const qmoe_linear_attrs* attrs,
                         const qmoe_tensor* output, const qmoe_tensor* preact, void* workspace, size_t workspace_bytes,
                         void* stream) {
-  if (!output) return QMOE_ERR_NULL;
-  LinPlan p;
-  qmoe_status st = check(input, weights, bias, offsets, preact, attrs, {residual, output}, &p);
-  if (st != QMOE_OK) return st;
-  if (p.M == 0 || p.N == 0) return QMOE_OK;
-  place_forward(&p);
-  const uintptr_t op = p.Kp == p.K ? 16 : (uintptr_t)p.es;
-  st = check_data({input, weights, bias, residual, output, preact}, p.es);
-  if (st == QMOE_OK) st = check_data({offsets}, 4);
-  if (st != QMOE_OK) return st;
-  if (!aligned_to(input->data, op) || !aligned_to(weights->data, op)) return QMOE_ERR_ALIGN;
-  st = check_ws(workspace, workspace_bytes, p.bytes);
-  if (st != QMOE_OK) return st;
+  return forward(input, weights, bias, residual, offsets, attrs, output, preact, nullptr, nullptr, 0, workspace,
+                 workspace_bytes, stream);
+}
 
-  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
-  LinearGemm g = base_gemm(p, input, weights, offsets);
-  g.bias = bias ? bias->data : nullptr;
-  g.res = residual ? residual->data : nullptr;
-  g.out = const_cast<void*>(output->data);
-  g.pre = preact ? const_cast<void*>(preact->data) : nullptr;
-  if (p.Kp != p.K) {
-    if (launch_linear_pad((int)p.es, {g.x, p.M, p.K, ws + p.off_x, p.Kp}, {g.w, wrows(p), p.K, ws + p.off_w, p.Kp}, s) !=
-        hipSuccess)
-      return QMOE_ERR_HIP;
-    g.x = ws + p.off_x;
-    g.w = ws + p.off_w;
-    g.ldx = g.ldw = p.Kp;
-  }
-  return run_product(p.type, LIN_FWD, p.fwd, g, reinterpret_cast<float*>(ws + p.off_partial), s) ? QMOE_OK
-                                                                                                : QMOE_ERR_HIP;
+qmoe_status qmoe_linear_q8_workspace_size(const qmoe_tensor* input, const qmoe_tensor* weights,
+                                          const qmoe_tensor* bias, const qmoe_tensor* residual,
+                                          const qmoe_tensor* offsets, const qmoe_linear_attrs* attrs,
+                                          const qmoe_tensor* output, const qmoe_tensor* codes,
+                                          const qmoe_tensor* scales, int64_t block_size, size_t* bytes) {
+  if (!bytes) return QMOE_ERR_NULL;
+  LinPlan p;
+  qmoe_status st = check(input, weights, bias, offsets, nullptr, attrs, {residual, output}, &p);
+  if (st == QMOE_OK && (codes || scales)) st = check_rows8(codes, scales, p.M, p.N, block_size);
+  if (st != QMOE_OK) return st;
+  place_forward(&p);
+  *bytes = p.bytes;
+  return QMOE_OK;
+}
+
+qmoe_status qmoe_linear_q8(const qmoe_tensor* input, const qmoe_tensor* weights, const qmoe_tensor* bias,
+                           const qmoe_tensor* residual, const qmoe_tensor* offsets, const qmoe_linear_attrs* attrs,
+                           const qmoe_tensor* output, const qmoe_tensor* codes, const qmoe_tensor* scales,
+                           int64_t block_size, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!codes || !scales) return QMOE_ERR_NULL;
+  return forward(input, weights, bias, residual, offsets, attrs, output, nullptr, codes, scales, block_size, workspace,
+                 workspace_bytes, stream);
 }
 
 qmoe_status qmoe_linear_backward_workspace_size(const qmoe_tensor* grad_output, const qmoe_tensor* input,
@@ -385,66 +507,41 @@ qmoe_status qmoe_linear_backward(const qmoe_tensor* grad_output, const qmoe_tens
                                  const qmoe_tensor* grad_weights, const qmoe_tensor* grad_bias, void* workspace,
                                  size_t workspace_bytes, void* stream) {
   LinPlan p;
-  qmoe_status st = check_grads(grad_output, input, weights, preact, offsets, attrs, grad_input, grad_weights,
-                               grad_bias, &p);
+  const qmoe_status st = check_grads(grad_output, input, weights, preact, offsets, attrs, grad_input, grad_weights,
+                                     grad_bias, &p);
   if (st != QMOE_OK) return st;
-  st = check_data({grad_output, input, weights, preact, grad_input, grad_weights, grad_bias}, p.es);
-  if (st == QMOE_OK) st = check_data({offsets}, 4);
-  if (st != QMOE_OK) return st;
-  const uintptr_t op = p.Kp == p.K ? 16 : (uintptr_t)p.es;
-  if (!aligned_to(input->data, op) || !aligned_to(weights->data, op)) return QMOE_ERR_ALIGN;
-  if (!needs_dz(p) && !aligned_to(grad_output->data, 16)) return QMOE_ERR_ALIGN;
-  st = check_ws(workspace, workspace_bytes, p.bytes);
-  if (st != QMOE_OK) return st;
+  return backward(p, grad_output, input, weights, preact, offsets, grad_input, grad_weights, grad_bias, Held{},
+                  workspace, workspace_bytes, stream);
+}
 
-  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
-  const bool gx = grad_input && p.M > 0 && p.K > 0;
-  const bool gw = grad_weights && p.G > 0 && p.N > 0 && p.K > 0;
-  const bool gb = grad_bias && p.G > 0 && p.N > 0;
-  LinearGemm g = base_gemm(p, input, weights, offsets);
-  g.dz = grad_output->data;
-  float* sums = gb ? reinterpret_cast<float*>(ws + p.off_sums) : nullptr;
-  const bool dz = (gx || gw) && needs_dz(p);
-  if (p.M > 0 && p.N > 0 && (dz || gb)) {
-    LinearActGrad a{};
-    a.dy = grad_output->data;
-    a.z = p.act.type == QMOE_ACT_IDENTITY ? nullptr : preact->data;
-    a.dz = dz ? ws + p.off_dz : nullptr;
-    a.lddz = p.Np;
-    a.sums = sums;
-    a.offsets = g.offsets;
-    a.G = g.G;
-    a.M = g.M;
-    a.N = g.N;
-    a.act = p.act;
-    if (launch_linear_act_grad(p.type, a, s) != hipSuccess) return QMOE_ERR_HIP;
-    if (dz) {
-      g.dz = ws + p.off_dz;
-      g.lddz = p.Np;
-    }
-  }
-  if (gb && launch_linear_bias_grad(p.type, sums, g.offsets, g.G, g.M, g.N, const_cast<void*>(grad_bias->data), s) !=
-                hipSuccess)
-    return QMOE_ERR_HIP;
-  float* partial = reinterpret_cast<float*>(ws + p.off_partial);
-  if (p.Kp != p.K) {
-    if (launch_linear_pad((int)p.es, {g.x, gw ? p.M : 0, p.K, ws + p.off_x, p.Kp},
-                          {g.w, gx ? wrows(p) : 0, p.K, ws + p.off_w, p.Kp}, s) != hipSuccess)
-      return QMOE_ERR_HIP;
-    g.x = ws + p.off_x;
-    g.w = ws + p.off_w;
-    g.ldx = g.ldw = p.Kp;
-  }
-  if (gx) {
-    g.out = const_cast<void*>(grad_input->data);
-    if (!run_product(p.type, LIN_DX, p.dx, g, partial, s)) return QMOE_ERR_HIP;
-  }
-  if (gw) {
-    g.out = const_cast<void*>(grad_weights->data);
-    if (!run_product(p.type, LIN_DW, p.dw, g, partial, s)) return QMOE_ERR_HIP;
-  }
+qmoe_status qmoe_linear_backward_q8_workspace_size(
+    const qmoe_tensor* grad_output, const qmoe_tensor* input, const qmoe_tensor* input_scales, const qmoe_tensor* perm,
+    const qmoe_tensor* weights, const qmoe_tensor* preact, const qmoe_tensor* preact_scales, int64_t block_size,
+    const qmoe_tensor* offsets, const qmoe_linear_attrs* attrs, const qmoe_tensor* grad_input,
+    const qmoe_tensor* grad_weights, const qmoe_tensor* grad_bias, size_t* bytes) {
+  if (!bytes) return QMOE_ERR_NULL;
+  LinPlan p;
+  const qmoe_status st = check_held(grad_output, input, weights, preact, offsets, attrs, grad_input, grad_weights,
+                                    grad_bias, {input_scales, preact_scales, perm, block_size}, &p);
+  if (st != QMOE_OK) return st;
+  *bytes = p.bytes;
   return QMOE_OK;
+}
+
+qmoe_status qmoe_linear_backward_q8(const qmoe_tensor* grad_output, const qmoe_tensor* input,
+                                    const qmoe_tensor* input_scales, const qmoe_tensor* perm,
+                                    const qmoe_tensor* weights, const qmoe_tensor* preact,
+                                    const qmoe_tensor* preact_scales, int64_t block_size, const qmoe_tensor* offsets,
+                                    const qmoe_linear_attrs* attrs, const qmoe_tensor* grad_input,
+                                    const qmoe_tensor* grad_weights, const qmoe_tensor* grad_bias, void* workspace,
+                                    size_t workspace_bytes, void* stream) {
+  const Held h{input_scales, preact_scales, perm, block_size};
+  LinPlan p;
+  const qmoe_status st = check_held(grad_output, input, weights, preact, offsets, attrs, grad_input, grad_weights,
+                                    grad_bias, h, &p);
+  if (st != QMOE_OK) return st;
+  return backward(p, grad_output, input, weights, preact, offsets, grad_input, grad_weights, grad_bias, h, workspace,
+                  workspace_bytes, stream);
 }
 
 }  // extern "C"

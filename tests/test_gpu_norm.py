@@ -1,0 +1,161 @@
+"""GPU parity of the root-mean-square norm and its gradients with the float64
+oracle, per element to bounds derived from the arithmetic: with u = 2^-24, a
+float32 sum of n products of one sign is within 2 (n + 1) u of itself, so 1 /
+sqrt(mean + eps) within (n + 8) u (half of the sum's, and a division, an
+addition, a root and a reciprocal of 2 u each at most); a result has two more
+products and its roundings."""
+import numpy as np
+import pytest
+
+import quantized_mixture_experts_router_amd as qm
+from oracle import front_oracle as F
+
+import front_util as V
+import steps_util as U
+
+pytestmark = pytest.mark.gpu
+
+TYPES = ["float32", "float16", "bfloat16"]
+u = 2.0 ** -24
+
+
+@pytest.fixture(scope="module")
+def torch():
+    import torch as _t
+    if not _t.cuda.is_available():
+        pytest.skip("no GPU")
+    return _t
+
+
+def check(torch, dt, M, H, residual=True, weight=True, fmt=None, block=128, output=True, eps=1e-6, scale=1.0, seed=0):
+    U.say(f"[norm {dt}] {M} x {H} residual={residual} weight={weight} {fmt} {block}")
+    r = np.random.default_rng(seed + M * H)
+    x, fx = U.typed(torch, r.standard_normal((M, H)) * scale, dt)
+    res, fr = U.typed(torch, r.standard_normal((M, H)) * scale if residual else None, dt)
+    w, fw = U.typed(torch, 1 + 0.1 * r.standard_normal(H) if weight else None, dt)
+    y, h, codes, scales = qm.rms_norm(x, w, res, eps, fmt, block, output)
+    torch.cuda.synchronize()
+    fh = fx
+    if residual:
+        # a float32 sum, rounded to the type
+        want = (x.float().cpu() + res.float().cpu()).to(x.dtype)
+        assert torch.equal(h.cpu(), want)
+        fh = want.double().numpy()
+    else:
+        assert h is None
+    ref = F.rms_norm(fh, fw, eps)
+    e = (H + 10) * u * np.abs(ref)
+    if output:
+        U.check(U.back(y), ref, U.rounded(dt, ref, e), "output")
+    else:
+        assert y is None
+    if fmt:
+        V.check_eight(torch, codes, scales, block, ref, e, "8 bits")
+    g, fg = U.typed(torch, r.standard_normal((M, H)), dt)
+    t = torch.from_numpy(fh).to(x.dtype).cuda()
+    gx, gw = qm.rms_norm_backward(g, t, w, res, eps)
+    rx, rw = F.rms_norm_grad(fg, fh, fw, fr, eps)
+    s = 1 / np.sqrt((fh ** 2).sum(1, keepdims=True) / H + eps)
+    gi = np.abs(fg) * (1 if fw is None else np.abs(fw))
+    # n = h s and the mean of g w n, both within (n + 12) u and sums of magnitudes; one subtraction, one product, one sum
+    mean = (gi * np.abs(fh) * s).sum(1, keepdims=True) / H
+    ex = (3 * H + 40) * u * s * (gi + np.abs(fh) * s * mean) + (0 if fr is None else 2 * u * np.abs(fr))
+    U.check(U.back(gx), rx, U.rounded(dt, rx, ex), "grad_input")
+    if weight:
+        A = (np.abs(fg) * np.abs(fh) * s).sum(0)
+        U.check(U.back(gw), rw, U.rounded(dt, rw, (H + 2 * M + 14) * u * A), "grad_weight")
+    else:
+        assert gw is None
+
+
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("M,H", [(1, 1), (1, 8), (3, 7), (5, 64), (2, 511), (17, 513), (4, 1000), (3, 2048), (2, 2049), (9, 4096),
+                                 (2, 8200), (3, 16384), (1, 16390), (2, 32776), (3, 33000)])
+def test_norm(torch, dt, M, H):
+    check(torch, dt, M, H, residual=H % 3 != 0, weight=H % 5 != 0)
+
+
+@pytest.mark.parametrize("block", V.BLOCKS)
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("dt", TYPES)
+def test_norm_in_8_bits(torch, dt, fmt, block):
+    check(torch, dt, 3, 264, fmt=fmt, block=block)
+    check(torch, dt, 2, 131, residual=False, weight=False, fmt=fmt, block=block, output=False)
+    check(torch, dt, 2, 1027, fmt=fmt, block=block, output=False)
+
+
+@pytest.mark.parametrize("dt,H", [("float32", 16400), ("float16", 33000), ("bfloat16", 32900)])
+def test_long_rows_in_8_bits(torch, dt, H):
+    check(torch, dt, 2, H, fmt="int8", block=128)
+    check(torch, dt, 2, H, residual=False, fmt="e4m3", block=16, output=False)
+
+
+@pytest.mark.parametrize("dt", TYPES)
+def test_many_rows(torch, dt):
+    check(torch, dt, 2100, 24, fmt="int8", block=16)
+    check(torch, dt, 700, 520)
+
+
+@pytest.mark.parametrize("scale,eps", [(1e-4, 1e-6), (100.0, 1e-5), (1e-3, 1e-12), (1.0, 10.0)])
+def test_magnitudes(torch, scale, eps):
+    check(torch, "float16" if scale > 1e-3 else "bfloat16", 4, 96, scale=scale, eps=eps)
+    check(torch, "float32", 4, 96, scale=scale, eps=eps, fmt="e4m3", block=32)
+
+
+@pytest.mark.parametrize("dt", TYPES)
+def test_zero_rows_and_what_is_not_finite(torch, dt):
+    t = getattr(torch, dt)
+    x = torch.ones(5, 72, dtype=t, device="cuda")
+    x[0] = 0
+    x[2, 3] = float("nan")
+    x[3, 71] = float("inf")
+    y, _, c, s = qm.rms_norm(x, None, None, 1e-6, "int8", 16)
+    assert not y[0].any() and (s[0] == 1).all() and (c[0] == 128).all()
+    assert y[2].isnan().all() and s[2].isnan().all()
+    assert y[3, 71].isnan() and s[3, 4].isnan()
+    assert torch.equal(y[1], y[4]) and y[1].isfinite().all() and torch.equal(c[1], c[4])  # no other row is touched
+    g = torch.ones_like(x)
+    gx, _ = qm.rms_norm_backward(g, x)
+    assert gx[1].isfinite().all() and torch.equal(gx[1], gx[4])
+    assert torch.allclose(gx[0].double(), torch.full((72,), 1000.0, device="cuda", dtype=torch.float64), rtol=2.0 ** -7)
+
+
+def test_empty(torch):
+    w = torch.ones(8, device="cuda")
+    x = torch.zeros(0, 8, device="cuda")
+    y, h, c, s = qm.rms_norm(x, w, x, format="int8")
+    assert y.shape == h.shape == c.shape == (0, 8) and s.shape == (0, 1)
+    gx, gw = qm.rms_norm_backward(x, x, w)
+    assert gx.shape == (0, 8) and torch.equal(gw, torch.zeros(8, device="cuda"))  # the sum over no rows
+    x = torch.zeros(3, 0, device="cuda")
+    assert qm.rms_norm(x, w[:0])[0].shape == (3, 0)
+    assert qm.rms_norm_backward(x, x, w[:0])[1].shape == (0,)
+
+
+def test_either_gradient_alone(torch):
+    r = np.random.default_rng(1)
+    for H in (40, 17000):
+        x, g, w = (torch.from_numpy(r.standard_normal(s)).float().cuda() for s in ((6, H), (6, H), (H,)))
+        gx, gw = qm.rms_norm_backward(g, x, w)
+        only = torch.empty_like(x)
+        qm.qmoe_rms_norm_backward(g, None, x, w, 1e-6, only, None)
+        assert torch.equal(only, gx)
+        need = qm.qmoe_rms_norm_backward_workspace_size(g, None, x, w, 1e-6, None, w)
+        only = torch.empty_like(w)
+        qm.qmoe_rms_norm_backward(g, None, x, w, 1e-6, None, only, torch.empty(need, dtype=torch.uint8, device="cuda"))
+        assert torch.equal(only, gw)
+
+
+@pytest.mark.parametrize("offset", [1, 5])
+def test_any_element_alignment(torch, offset):
+    r = np.random.default_rng(offset)
+    M, H = 5, 264
+    buf = [torch.from_numpy(r.standard_normal(M * H + 16)).bfloat16().cuda() for _ in range(4)]
+    x, res, g, out = (b[offset:offset + M * H].view(M, H) for b in buf)
+    w = torch.from_numpy(r.standard_normal(H + 8)).bfloat16().cuda()[offset:offset + H]
+    keep = buf[3].clone()
+    qm.qmoe_rms_norm(x, res, w, 1e-6, None, out)
+    assert torch.equal(out, qm.rms_norm(x.clone(), w.clone(), res.clone())[0])
+    assert torch.equal(buf[3][:offset], keep[:offset]) and torch.equal(buf[3][offset + M * H:], keep[offset + M * H:])
+    a, b = qm.rms_norm_backward(g, x, w, res), qm.rms_norm_backward(g.clone(), x.clone(), w.clone(), res.clone())
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
