@@ -4,21 +4,47 @@
 #include "common.hpp"
 #include "launches.h"
 #include "route_scored.h"
+#include "wave.hpp"
 
 namespace qmoe {
 
 namespace {
 
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
-  return v;
+// Signed integers that order like the floats (which are not NaN and no -0).
+__device__ __forceinline__ int key_of(float v) {
+  const int b = __float_as_int(v);
+  return b ^ ((b >> 31) & 0x7fffffff);
 }
-template <typename V>
-__device__ __forceinline__ V wave_sum(V v) {
+__device__ __forceinline__ float of_key(int k) { return __int_as_float(k ^ ((k >> 31) & 0x7fffffff)); }
+constexpr int kNone = (int)0x807fffff;  // -infinity
+
+// x[j] <- e^x[j] for x <= 0 in 64 bits, within 2^-50 of itself (the series to r^12
+// over |r| <= ln 2 / 2); below -110, where float32 has only 0, it stays at e^-110.
+template <int V>
+__device__ __forceinline__ void exp_below(double (&x)[V]) {
+  constexpr double c[] = {1.0 / 39916800.0, 1.0 / 3628800.0, 1.0 / 362880.0, 1.0 / 40320.0, 1.0 / 5040.0, 1.0 / 720.0,
+                          1.0 / 120.0,      1.0 / 24.0,      1.0 / 6.0,      0.5,           1.0,          1.0};
+  double n[V], p[V];
 #pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o);
-  return v;
+  for (int j = 0; j < V; ++j) {
+    x[j] = x[j] < -110.0 ? -110.0 : x[j];
+    n[j] = __builtin_rint(x[j] * 1.4426950408889634);
+    x[j] = fma(n[j], -0.6931471805599453, x[j]);
+    x[j] = fma(n[j], -2.3190468138462996e-17, x[j]);
+    p[j] = 1.0 / 479001600.0;
+  }
+#pragma unroll
+  for (int i = 0; i < 12; ++i)
+#pragma unroll
+    for (int j = 0; j < V; ++j) p[j] = fma(p[j], x[j], c[i]);
+#pragma unroll
+  for (int j = 0; j < V; ++j) x[j] = __builtin_ldexp(p[j], (int)n[j]);
+}
+// 1 / d for normal d, within 2^-51 of itself: the hardware's estimate (2^-23 at least) and two steps of Newton's method.
+__device__ __forceinline__ double reciprocal(double d) {
+  double y = __builtin_amdgcn_rcp(d);
+  y = fma(y, fma(-d, y, 1.0), y);
+  return fma(y, fma(-d, y, 1.0), y);
 }
 
 // A row's logits, lane + 64 j: +infinity counts as the largest float, -infinity
@@ -36,119 +62,152 @@ __device__ __forceinline__ void load_logits(const float* __restrict__ row, int E
 // evaluated in 64 bits and rounded once to float32: an expert is selected by
 // comparing its score plus bias with others', and two that differ in float32's
 // last bits would change places with the rounding errors of a float32 exponential.
-template <int V>
+//
+// Bound by the vector instructions: reductions stay in registers, ranks of groups
+// are counted by all lanes, and a round of the selection is one reduction, a compare
+// a register (whose ballots give the lowest expert that holds the largest key) and
+// a write to one lane.  16384 x 256 logits, 6 of 16 groups' 5, softmax: FIGURES
+// k <= 64 (else MANY: pick r in lane r % 64 of register r / 64).
+template <int V, bool MANY>
 __global__ void __launch_bounds__(256) qmoe_route_scored(const float* __restrict__ logits,
                                                          const float* __restrict__ bias, int T, RouteScored a, int b0,
                                                          int* __restrict__ idx, float* __restrict__ w) {
-  __shared__ float sc[4][64 * V];
+  __shared__ float lds[4][64 * V];
   const int wave = threadIdx.x >> 6, lane = lane_id();
   const int t = (b0 + blockIdx.x) * 4 + wave;
   if (t >= T) return;
-  float v[V], p[V], c[V];
+  float v[V], p[V], b[V];
   load_logits<V>(logits + (long)t * a.E, a.E, lane, v);
+#pragma unroll
+  for (int j = 0; j < V; ++j) b[j] = bias && lane + 64 * j < a.E ? bias[lane + 64 * j] : 0.f;
+  double e[V];
   if (a.sigmoid) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) p[j] = (float)(1.0 / (1.0 + exp(-(double)v[j])));
-  } else {
-    float m = v[0];
+    for (int j = 0; j < V; ++j) e[j] = -fabs((double)v[j]);
+    exp_below<V>(e);
 #pragma unroll
-    for (int j = 1; j < V; ++j) m = fmaxf(m, v[j]);
-    m = wave_max(m);
-    if (m == -INFINITY) m = 0.f;
-    double e[V], sum = 0.0;
+    for (int j = 0; j < V; ++j) p[j] = (float)((v[j] < 0.f ? e[j] : 1.0) * reciprocal(1.0 + e[j]));
+  } else {
+    int m = key_of(v[0]);
+#pragma unroll
+    for (int j = 1; j < V; ++j) m = max(m, key_of(v[j]));
+    // (a row that is all masked: nothing is selected, whatever the scores are)
+    const double top = (double)fmaxf(of_key(wave_max_int(m)), -3.4028234664e38f);
+#pragma unroll
+    for (int j = 0; j < V; ++j) e[j] = (double)v[j] - top;
+    exp_below<V>(e);
+    double sum = 0.0;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      e[j] = exp((double)v[j] - (double)m);
+      e[j] = v[j] == -INFINITY ? 0.0 : e[j];
       sum += e[j];
     }
-    sum = wave_sum(sum);
+    // (the largest one's e is 1)
+    const double inv = reciprocal(fmax(wave_sum_double(sum), 1.0));
 #pragma unroll
-    for (int j = 0; j < V; ++j) p[j] = (float)(e[j] / sum);
+    for (int j = 0; j < V; ++j) p[j] = (float)(e[j] * inv);
   }
+  int c[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    c[j] = p[j];
-    if (bias && lane + 64 * j < a.E) c[j] += bias[lane + 64 * j];
-    c[j] = v[j] == -INFINITY || c[j] != c[j] ? -INFINITY : c[j];
+    const float x = p[j] + b[j];
+    c[j] = v[j] == -INFINITY || x != x ? kNone : key_of(x);
   }
   if (a.kept < a.groups) {
-    float* s = sc[wave];
+    int* s = reinterpret_cast<int*>(lds[wave]);
 #pragma unroll
     for (int j = 0; j < V; ++j) s[lane + 64 * j] = c[j];
     // (one wavefront's own LDS words: written and read in program order)
     __builtin_amdgcn_wave_barrier();
     // 2^log lanes a group find its two largest
     const int per = a.E / a.groups, log = 31 - __clz(64 / a.groups), L = 1 << log;
-    const int g = lane >> log;
-    float first = -INFINITY, second = -INFINITY;
+    const int g = lane >> log, sub = lane & (L - 1);
+    int first = kNone, second = kNone;
     if (g < a.groups) {
-      for (int i = lane & (L - 1); i < per; i += L) {
-        const float x = s[g * per + i];
-        second = fmaxf(second, fminf(first, x));
-        first = fmaxf(first, x);
+      for (int i = sub; i < per; i += L) {
+        const int x = s[g * per + i];
+        second = max(second, min(first, x));
+        first = max(first, x);
       }
     }
-    for (int o = 1; o < L; o <<= 1) {
-      const float f = __shfl_xor(first, o), q = __shfl_xor(second, o);
-      second = fmaxf(fmaxf(second, q), fminf(first, f));
-      first = fmaxf(first, f);
-    }
-    const float score = a.group_top == 2 && second > -INFINITY ? first + second : first;
-    // a group stays if fewer than `kept` are larger, or equal and in front of it
+    auto join = [&](uint32_t f, uint32_t q) {
+      second = max(max(second, (int)q), min(first, (int)f));
+      first = max(first, (int)f);
+    };
+    if (log > 0) join(dpp_from<kDppXor1>(first), dpp_from<kDppXor1>(second));
+    if (log > 1) join(dpp_from<kDppXor2>(first), dpp_from<kDppXor2>(second));
+    if (log > 2) join(dpp_from<kDppHalf>(first), dpp_from<kDppHalf>(second));
+    if (log > 3) join(dpp_from<kDppRow>(first), dpp_from<kDppRow>(second));
+    if (log > 4) join(__shfl_xor(first, 16), __shfl_xor(second, 16));
+    const int score = a.group_top == 2 && second > kNone ? key_of(of_key(first) + of_key(second)) : first;
+    // a group stays if fewer than `kept` are larger, or equal and in front of it: a group's lanes share the others
+    __builtin_amdgcn_wave_barrier();
+    if (sub == 0 && g < a.groups) s[g] = score;
+    __builtin_amdgcn_wave_barrier();
     int before = 0;
-    for (int q = 0; q < a.groups; ++q) {
-      const float o = __shfl(score, q << log);
-      before += o > score || (o == score && q < g);
-    }
+    for (int q = sub; q < a.groups; q += L) before += s[q] > score - (q < g);
+    if (log > 0) before += dpp_from<kDppXor1>(before);
+    if (log > 1) before += dpp_from<kDppXor2>(before);
+    if (log > 2) before += dpp_from<kDppHalf>(before);
+    if (log > 3) before += dpp_from<kDppRow>(before);
+    if (log > 4) before += __shfl_xor(before, 16);
     const unsigned long long stays = __ballot(before < a.kept);
+    // (e / per by a product: exact for e < 1024 and per <= 1024)
+    const uint32_t by = (1u << 20) / (uint32_t)per + 1u;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const int e = lane + 64 * j;
-      if (e < a.E && !(stays >> ((e / per) << log) & 1ull)) c[j] = -INFINITY;
+      const int x = lane + 64 * j;
+      if (x < a.E && !(stays >> (((x * by) >> 20) << log) & 1ull)) c[j] = kNone;
     }
+    __builtin_amdgcn_wave_barrier();
   }
-  // pick r waits in lane r % 64 of register r / 64
-  float pv[V], sum = 0.f;
-  int pe[V];
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    pv[j] = 0.f;
-    pe[j] = -1;
-  }
-  for (int r = 0; r < a.k; ++r) {
-    float m = c[0];
+  for (int j = 0; j < V; ++j) lds[wave][lane + 64 * j] = p[j];
+  constexpr int KV = MANY ? V : 1;
+  int pe[KV];
 #pragma unroll
-    for (int j = 1; j < V; ++j) m = fmaxf(m, c[j]);
-    m = wave_max(m);
-    if (m == -INFINITY) break;  // only masked experts are left
-    int e = -1;
-    float at = 0.f;
+  for (int j = 0; j < KV; ++j) pe[j] = -1;
+  auto largest = [&]() {
+    int m = c[0];
+#pragma unroll
+    for (int j = 1; j < V; ++j) m = max(m, c[j]);
+    return __builtin_amdgcn_readfirstlane(wave_max_int(m));
+  };
+  int m = largest();
+  for (int r = 0; r < a.k && m != kNone; ++r) {  // (kNone: only masked experts are left)
+    bool found = false;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const unsigned long long b = __ballot(c[j] == m);
-      if (e < 0 && b) {
-        const int l = __ffsll((long long)b) - 1;
-        e = l + 64 * j;
-        at = __shfl(p[j], l);
-        if (lane == l) c[j] = -INFINITY;
+      const unsigned long long at = __ballot(c[j] == m);
+      if (!found && at) {
+        const int l = __ffsll((long long)at) - 1;
+        c[j] = lane == l ? kNone : c[j];
+        found = true;
+#pragma unroll
+        for (int i = 0; i < KV; ++i)
+          if (i == r >> 6) pe[i] = lane == (r & 63) ? l + 64 * j : pe[i];
       }
     }
-    sum += at;
+    m = largest();
+  }
+  __builtin_amdgcn_wave_barrier();
+  float x[KV], sum = 0.f;
 #pragma unroll
-    for (int j = 0; j < V; ++j)
-      if (r == lane + 64 * j) {
-        pv[j] = at;
-        pe[j] = e;
-      }
+  for (int j = 0; j < KV; ++j) {
+    x[j] = pe[j] < 0 ? 0.f : lds[wave][pe[j]];
+    sum += x[j];
+  }
+  if (a.normalize) {
+    sum = wave_sum_float(sum);
+#pragma unroll
+    for (int j = 0; j < KV; ++j) x[j] = sum > 0.f ? x[j] / sum : 0.f;
   }
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
+  for (int j = 0; j < KV; ++j) {
     const int r = lane + 64 * j;
     if (r < a.k) {
-      float x = pv[j];
-      if (a.normalize) x = sum > 0.f ? x / sum : 0.f;
       idx[(long)t * a.k + r] = pe[j];
-      w[(long)t * a.k + r] = x * a.scale;
+      w[(long)t * a.k + r] = x[j] * a.scale;
     }
   }
 }
@@ -177,14 +236,15 @@ __global__ void __launch_bounds__(256) qmoe_route_scored_grad(const float* __res
   load_logits<V>(row, a.E, lane, v);
   float top = 0.f, inv = 1.f;
   if (!a.sigmoid) {
-    float m = v[0], sum = 0.f;
+    int m = key_of(v[0]);
+    float sum = 0.f;
 #pragma unroll
-    for (int j = 1; j < V; ++j) m = fmaxf(m, v[j]);
-    m = wave_max(m);
-    top = m == -INFINITY ? 0.f : m;
+    for (int j = 1; j < V; ++j) m = max(m, key_of(v[j]));
+    m = wave_max_int(m);
+    top = m == kNone ? 0.f : of_key(m);
 #pragma unroll
     for (int j = 0; j < V; ++j) sum += expf(v[j] - top);
-    sum = wave_sum(sum);
+    sum = wave_sum_float(sum);
     inv = sum > 0.f ? 1.f / sum : 0.f;
   }
   // (sigmoid: e^-|l| keeps the digits of scores near 0 and of 1 - s near 1)
@@ -209,8 +269,8 @@ __global__ void __launch_bounds__(256) qmoe_route_scored_grad(const float* __res
     S += u;
     dot = fmaf(u, g, dot);
   }
-  S = wave_sum(S);
-  dot = wave_sum(dot);
+  S = wave_sum_float(S);
+  dot = wave_sum_float(dot);
   float shift = 0.f, mean = dot;
   if (a.normalize) {
     shift = S > 0.f ? dot / S : 0.f;
@@ -243,6 +303,15 @@ __global__ void __launch_bounds__(256) qmoe_route_scored_grad(const float* __res
   }
 }
 
+template <int V>
+void go_scored(dim3 grid, hipStream_t st, const float* logits, const float* bias, int T, const RouteScored& a, int b0,
+               int* idx, float* w) {
+  if (a.k <= 64)
+    hipLaunchKernelGGL((qmoe_route_scored<V, false>), grid, dim3(256), 0, st, logits, bias, T, a, b0, idx, w);
+  else
+    hipLaunchKernelGGL((qmoe_route_scored<V, true>), grid, dim3(256), 0, st, logits, bias, T, a, b0, idx, w);
+}
+
 }  // namespace
 
 #define QMOE_BY_REGS(CALL)                                  \
@@ -258,8 +327,8 @@ __global__ void __launch_bounds__(256) qmoe_route_scored_grad(const float* __res
 hipError_t launch_route_scored(const float* logits, const float* bias, int T, const RouteScored& a, int* idx, float* w,
                                hipStream_t st) {
   return in_launches(((long)T + 3) / 4, [&](int b0, unsigned n) {
-    const dim3 grid(n), block(256);
-#define QMOE_CALL(VV) hipLaunchKernelGGL(qmoe_route_scored<VV>, grid, block, 0, st, logits, bias, T, a, b0, idx, w)
+    const dim3 grid(n);
+#define QMOE_CALL(VV) go_scored<VV>(grid, st, logits, bias, T, a, b0, idx, w)
     QMOE_BY_REGS(QMOE_CALL)
 #undef QMOE_CALL
   });
