@@ -323,13 +323,46 @@ __device__ __forceinline__ void linear_rows8(const LinearGemm& g, const float (&
       top = max(top, abs_bits(v[i]));
     }
     top = lanes_max(top, bl - (W == 4 ? 2 : 1));
-    const uint32_t s = g.pre8.format == R8_INT8 ? r8_scale_bits<R8_INT8>(top) : r8_scale_bits<R8_E4M3>(top);
+    const uint32_t s = r8_scale_bits(g.pre8.format, top);
     if (!ok[r] || n <= 0) continue;
     uint8_t* p = g.pre8.codes + (long)m[r] * g.N + c;
     if (g.pre8.format == R8_INT8) store_codes<R8_INT8, W>(p, n, v, r8_inverse(s));
     else store_codes<R8_E4M3, W>(p, n, v, r8_inverse(s));
     if ((c & ((1 << bl) - 1)) == 0) g.pre8.scales[(long)m[r] * blocks + (c >> bl)] = __uint_as_float(s);
   }
+}
+
+// The same of sixteen columns c .. of row m a thread, from the float32 sums of an
+// output tile in LDS at `sums`, without their bias b.  A lane takes its four
+// 16-byte pieces in the order i ^ swz (b lies in that order too), so that lanes
+// 256 bytes apart meet different banks.
+__device__ __forceinline__ void linear_codes16(const Rows8& q, int N, const char* sums, const f32x4 (&b)[4], int swz,
+                                               int c, long m, bool ok) {
+  f32x4 v[4];
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[i] = *(const f32x4*)(sums + ((i ^ swz) << 4)) + b[i];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) top = max(top, abs_bits(v[i][k]));
+  }
+  const int bl = q.block_log;
+  const uint32_t s = r8_scale_bits(q.format, lanes_max(top, bl - 4));
+  const float inv = r8_inverse(s);
+  u32x4 u;
+  if (q.format == R8_INT8) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u[i] = r8_encode4<R8_INT8>(v[i], inv);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u[i] = r8_encode4<R8_E4M3>(v[i], inv);
+  }
+  if (swz & 1) u = u32x4{u[1], u[0], u[3], u[2]};
+  if (swz & 2) u = u32x4{u[2], u[3], u[0], u[1]};
+  const int n = N - c;
+  if (!ok || n <= 0) return;
+  store_piece<uint8_t, 16>(q.codes + m * N + c, n, __builtin_bit_cast(RowPiece<uint8_t, 16>::type, u));
+  if ((c & ((1 << bl) - 1)) == 0) q.scales[m * ((N + (1 << bl) - 1) >> bl) + (c >> bl)] = __uint_as_float(s);
 }
 
 // Zeros in 8 bits in the four columns from n on of row m.

@@ -12,40 +12,45 @@
 #pragma once
 #include <type_traits>
 
-#include "common.hpp"
 #include "rows8.h"
+#include "wave.hpp"
 
 namespace qmoe {
 
 // Bits of the scale from the bits of m (which order like the magnitudes, NaN above infinity).
-template <int F>
-__device__ __forceinline__ uint32_t r8_scale_bits(uint32_t m) {
+__device__ __forceinline__ uint32_t r8_scale_bits(int format, uint32_t m) {
   // m = 2^x 1.f: e = x - 6 unless 1.f >= 1.9921875 (int8), x - 8 unless 1.f > 1.8125 (e4m3): the sum carries into the exponent then
-  const int b = F == R8_INT8 ? (int)((m + 0x010000u) >> 23) - 6 : (int)((m + 0x17ffffu) >> 23) - 8;
-  uint32_t s = (uint32_t)max(b, 1) << 23;
+  const uint32_t carry = format == R8_INT8 ? 0x010000u : 0x17ffffu;
+  const int below = format == R8_INT8 ? 6 : 8;
+  uint32_t s = (uint32_t)max((int)((m + carry) >> 23) - below, 1) << 23;
   s = m == 0u ? 0x3f800000u : s;
   return m >= 0x7f800000u ? 0x7fc00000u : s;
 }
-// 1 / scale (0 for NaN: whatever the codes are, their values are NaN).
-__device__ __forceinline__ float r8_inverse(uint32_t scale_bits) {
-  return scale_bits >= 0x7f800000u ? 0.f : __uint_as_float(0x7f000000u - scale_bits);
+template <int F>
+__device__ __forceinline__ uint32_t r8_scale_bits(uint32_t m) {
+  return r8_scale_bits(F, m);
 }
+// 1 / scale (any number where that is NaN: whatever the codes are, their values are NaN).
+__device__ __forceinline__ float r8_inverse(uint32_t scale_bits) { return __uint_as_float(0x7f000000u - scale_bits); }
 
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
-template <int CTRL>
-__device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
-  const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, CTRL, 0xf, 0xf, false);
-  return max(v, o);
-}
 // Largest of the 2^log lanes that differ in the low bits (log uniform, up to 6; every lane active).
 __device__ __forceinline__ uint32_t lanes_max(uint32_t v, int log) {
-  if (log > 0) v = dpp_max<0xb1>(v);   // quad_perm [1, 0, 3, 2]
-  if (log > 1) v = dpp_max<0x4e>(v);   // quad_perm [2, 3, 0, 1]
-  if (log > 2) v = dpp_max<0x141>(v);  // row_half_mirror: the other four of eight
-  if (log > 3) v = dpp_max<0x140>(v);  // row_mirror: the other eight of sixteen
-  if (log > 4) v = max(v, (uint32_t)__shfl_xor((int)v, 16));
-  if (log > 5) v = max(v, (uint32_t)__shfl_xor((int)v, 32));
+  if (log > 0) v = max(v, dpp_from<kDppXor1>(v));
+  if (log > 1) v = max(v, dpp_from<kDppXor2>(v));
+  if (log > 2) v = max(v, dpp_from<kDppHalf>(v));
+  if (log > 3) v = max(v, dpp_from<kDppRow>(v));
+  if (log > 4) {
+    uint32_t o = v;
+    swap16(v, o);
+    v = max(v, o);
+  }
+  if (log > 5) {
+    uint32_t o = v;
+    swap32(v, o);
+    v = max(v, o);
+  }
   return v;
 }
 
@@ -122,6 +127,11 @@ __device__ __forceinline__ void store_piece(ET* p, int n, typename RowPiece<ET, 
 #pragma unroll
   for (int i = 0; i < W; ++i)
     if (i < n) p[i] = t[i];
+}
+
+template <int F>
+__device__ __forceinline__ uint32_t r8_encode4(const f32x4& v, float inv) {
+  return r8_encode4<F>(v[0], v[1], v[2], v[3], inv);
 }
 
 // Codes of W (2, 4 or 8) values behind p, n of them in the row.
