@@ -11,29 +11,50 @@ namespace qmoe {
 
 namespace {
 
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o);
+// Sum over the TPR lanes (8, 16, 32 or 64) of a row.
+template <int TPR>
+__device__ __forceinline__ float lanes_sum(float v) {
+  auto add = [](float x, uint32_t y) { return x + __uint_as_float(y); };
+  v = add(v, dpp_from<kDppXor1>(__float_as_uint(v)));
+  v = add(v, dpp_from<kDppXor2>(__float_as_uint(v)));
+  v = add(v, dpp_from<kDppHalf>(__float_as_uint(v)));
+  if constexpr (TPR > 8) v = add(v, dpp_from<kDppRow>(__float_as_uint(v)));
+  if constexpr (TPR > 16) {
+    uint32_t x = __float_as_uint(v), y = x;
+    swap16(x, y);
+    v = add(__uint_as_float(x), y);
+  }
+  if constexpr (TPR > 32) {
+    uint32_t x = __float_as_uint(v), y = x;
+    swap32(x, y);
+    v = add(__uint_as_float(x), y);
+  }
   return v;
 }
 
-// Sums of N values over a workgroup of NW wavefronts, the same bits in every
-// thread; red: [2][NW][N], the caller alternates turn (one barrier a call).
-template <int N, int NW>
-__device__ __forceinline__ void block_sum(float (&v)[N], float (*red)[NW][N], int turn) {
+// Rows of a workgroup that gives TPR threads to each: 256 threads, or one row.
+constexpr int rows_of(int TPR) { return TPR < 256 ? 256 / TPR : 1; }
+constexpr int threads_of(int TPR) { return TPR < 256 ? 256 : TPR; }
+
+// Sums of N values over the TPR threads of a row, the same bits in every one;
+// red: [2][wavefronts][N] for rows of several wavefronts, where the caller
+// alternates turn (one barrier a call).
+template <int N, int TPR>
+__device__ __forceinline__ void row_sum(float (&v)[N], float (*red)[threads_of(TPR) / 64][N], int turn) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
-  if constexpr (NW > 1) {
+  for (int i = 0; i < N; ++i) v[i] = lanes_sum<TPR < 64 ? TPR : 64>(v[i]);
+  if constexpr (TPR > 64) {
     if (lane_id() == 0) {
 #pragma unroll
       for (int i = 0; i < N; ++i) red[turn][threadIdx.x >> 6][i] = v[i];
     }
     __syncthreads();
+    const int first = threadIdx.x / TPR * (TPR / 64);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      v[i] = red[turn][0][i];
+      v[i] = red[turn][first][i];
 #pragma unroll
-      for (int k = 1; k < NW; ++k) v[i] += red[turn][k][i];
+      for (int k = 1; k < TPR / 64; ++k) v[i] += red[turn][first + k][i];
     }
   }
 }
@@ -46,11 +67,11 @@ __device__ __forceinline__ void add_piece(typename RowPiece<ET, W>::type& x, con
   for (int i = 0; i < W; ++i) x[i] = (ET)((float)x[i] + (float)r[i]);
 }
 
-// y of a piece into the outputs: rounded once to the type, and (every lane of
-// the wavefront) once to 8 bits.
+// y of a piece into the outputs: rounded once to the type, and (every lane of a
+// row of 2^lanes lanes) once to 8 bits.
 template <typename ET, int F, int W>
-__device__ __forceinline__ void put_piece(const Norm& a, long m, int c, const float (&y)[W]) {
-  const int n = a.H - c;
+__device__ __forceinline__ void put_piece(const Norm& a, long m, int c, const float (&y)[W], int lanes = 6) {
+  const int n = m < a.M ? a.H - c : 0;
   if (a.y && n > 0) {
     typename RowPiece<ET, W>::type o;
 #pragma unroll
@@ -62,7 +83,7 @@ __device__ __forceinline__ void put_piece(const Norm& a, long m, int c, const fl
     uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < W; ++i) top = max(top, abs_bits(y[i]));
-    const uint32_t s = r8_scale_bits<F>(lanes_max(top, bl - (W == 8 ? 3 : 2)));
+    const uint32_t s = r8_scale_bits<F>(lanes_max(top, min(bl - (W == 8 ? 3 : 2), lanes)));
     if (n > 0) {
       store_codes<F, W>(a.q.codes + m * a.H + c, n, y, r8_inverse(s));
       if ((c & ((1 << bl) - 1)) == 0) a.q.scales[m * ((a.H + (1 << bl) - 1) >> bl) + (c >> bl)] = __uint_as_float(s);
@@ -70,42 +91,47 @@ __device__ __forceinline__ void put_piece(const Norm& a, long m, int c, const fl
   }
 }
 
-// A workgroup per row, NP pieces of 16 bytes a thread; it goes on to further
-// rows with the weight in registers.
-template <typename ET, int F, int NP, int TPB>
-__global__ void __launch_bounds__(TPB) qmoe_rms_norm(const Norm a) {
-  constexpr int W = 16 / (int)sizeof(ET), NW = TPB / 64;
+// TPR threads a row, NP pieces of 16 bytes each; a workgroup of 256 threads or
+// more takes a row, or several, and goes on to further ones with the weight in
+// registers.  Bfloat16 with residual: 8192 x 4096 49 us for 268 MB (5.4 TB/s), with
+// 8 bits beside it 58 us for 303 MB; 65536 x 64 8 us (a wavefront a row: 20 us).
+template <typename ET, int F, int NP, int TPR>
+__global__ void __launch_bounds__(threads_of(TPR)) qmoe_rms_norm(const Norm a) {
+  constexpr int W = 16 / (int)sizeof(ET), R = rows_of(TPR);
+  constexpr int kLanes = TPR >= 64 ? 6 : TPR == 32 ? 5 : TPR == 16 ? 4 : 3;
   using P = typename RowPiece<ET, W>::type;
-  __shared__ float red[2][NW][1];
-  const int c0 = threadIdx.x * W;
+  __shared__ float red[2][threads_of(TPR) / 64][1];
+  const int c0 = threadIdx.x % TPR * W;
   P w[NP];
 #pragma unroll
   for (int j = 0; j < NP; ++j) {
-    const int c = c0 + j * TPB * W;
+    const int c = c0 + j * TPR * W;
 #pragma unroll
     for (int i = 0; i < W; ++i) w[j][i] = (ET)1.f;
     if (a.w) w[j] = load_piece<ET, W>(static_cast<const ET*>(a.w) + c, a.H - c);
   }
   int turn = 0;
-  for (long m = blockIdx.x; m < a.M; m += gridDim.x, turn ^= 1) {
+  for (long m0 = (long)blockIdx.x * R; m0 < a.M; m0 += (long)gridDim.x * R, turn ^= 1) {
+    const long m = m0 + threadIdx.x / TPR;
+    const int H = m < a.M ? a.H : 0;
     P h[NP];
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
-      const int c = c0 + j * TPB * W;
-      h[j] = load_piece<ET, W>(static_cast<const ET*>(a.x) + m * a.H + c, a.H - c);
+      const int c = c0 + j * TPR * W;
+      h[j] = load_piece<ET, W>(static_cast<const ET*>(a.x) + m * a.H + c, H - c);
     }
     if (a.r) {
       P r[NP];
 #pragma unroll
       for (int j = 0; j < NP; ++j) {
-        const int c = c0 + j * TPB * W;
-        r[j] = load_piece<ET, W>(static_cast<const ET*>(a.r) + m * a.H + c, a.H - c);
+        const int c = c0 + j * TPR * W;
+        r[j] = load_piece<ET, W>(static_cast<const ET*>(a.r) + m * a.H + c, H - c);
       }
 #pragma unroll
       for (int j = 0; j < NP; ++j) {
-        const int c = c0 + j * TPB * W;
+        const int c = c0 + j * TPR * W;
         add_piece<ET, W>(h[j], r[j]);
-        if (a.sum) store_piece<ET, W>(static_cast<ET*>(a.sum) + m * a.H + c, a.H - c, h[j]);
+        if (a.sum) store_piece<ET, W>(static_cast<ET*>(a.sum) + m * a.H + c, H - c, h[j]);
       }
     }
     float ss[1] = {0.f};
@@ -113,22 +139,22 @@ __global__ void __launch_bounds__(TPB) qmoe_rms_norm(const Norm a) {
     for (int j = 0; j < NP; ++j)
 #pragma unroll
       for (int i = 0; i < W; ++i) ss[0] = fmaf((float)h[j][i], (float)h[j][i], ss[0]);
-    block_sum<1, NW>(ss, red, turn);
+    row_sum<1, TPR>(ss, red, turn);
     const float s = 1.f / sqrtf(ss[0] / (float)a.H + a.eps);
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
       float y[W];
 #pragma unroll
       for (int i = 0; i < W; ++i) y[i] = (float)h[j][i] * s * (float)w[j][i];
-      put_piece<ET, F, W>(a, m, c0 + j * TPB * W, y);
+      put_piece<ET, F, W>(a, m, c0 + j * TPR * W, y, kLanes);
     }
   }
 }
 
-// Rows too long for registers: read twice.
+// Rows too long for registers: read twice.  512 x 40000 bfloat16: 44 us for 164 MB.
 template <typename ET, int F>
 __global__ void __launch_bounds__(1024) qmoe_rms_norm_long(const Norm a) {
-  constexpr int W = 16 / (int)sizeof(ET), TPB = 1024;
+  constexpr int W = 16 / (int)sizeof(ET), TPR = 1024;
   using P = typename RowPiece<ET, W>::type;
   __shared__ float red[2][16][1];
   const int c0 = threadIdx.x * W;
@@ -140,16 +166,16 @@ __global__ void __launch_bounds__(1024) qmoe_rms_norm_long(const Norm a) {
   int turn = 0;
   for (long m = blockIdx.x; m < a.M; m += gridDim.x, turn ^= 1) {
     float ss[1] = {0.f};
-    for (int c = c0; c < a.H; c += TPB * W) {
+    for (int c = c0; c < a.H; c += TPR * W) {
       const P h = piece(m, c);
       if (a.sum && a.r) store_piece<ET, W>(static_cast<ET*>(a.sum) + m * a.H + c, a.H - c, h);
 #pragma unroll
       for (int i = 0; i < W; ++i) ss[0] = fmaf((float)h[i], (float)h[i], ss[0]);
     }
-    block_sum<1, 16>(ss, red, turn);
+    row_sum<1, TPR>(ss, red, turn);
     const float s = 1.f / sqrtf(ss[0] / (float)a.H + a.eps);
     // (every lane of a wavefront takes part in its blocks' largest magnitude)
-    for (int base = 0; base < a.H; base += TPB * W) {
+    for (int base = 0; base < a.H; base += TPR * W) {
       const int c = base + c0;
       float y[W] = {};
       if (c < a.H) {
@@ -164,19 +190,21 @@ __global__ void __launch_bounds__(1024) qmoe_rms_norm_long(const Norm a) {
   }
 }
 
-// A workgroup per row at a time; the weight's gradient of its rows stays in
-// registers and leaves as one row of partial sums.
-template <typename ET, int NP, int TPB>
-__global__ void __launch_bounds__(TPB) qmoe_rms_norm_grad(const NormGrad a, long ldp) {
-  constexpr int W = 16 / (int)sizeof(ET), NW = TPB / 64;
+// 8192 x 4096 bfloat16 with a gradient at the sum: 44 us for 268 MB and the partial
+// sums, 6.1 TB/s (inputs in part still in the last level of cache), 65536 x 64 10 us.
+// Threads and rows as above; the weight's gradient of a workgroup's rows stays
+// in registers and leaves as one row of partial sums.
+template <typename ET, int NP, int TPR>
+__global__ void __launch_bounds__(threads_of(TPR)) qmoe_rms_norm_grad(const NormGrad a, long ldp) {
+  constexpr int W = 16 / (int)sizeof(ET), R = rows_of(TPR);
   using P = typename RowPiece<ET, W>::type;
-  __shared__ float red[2][NW][2];
-  const int c0 = threadIdx.x * W;
+  __shared__ float red[2][threads_of(TPR) / 64][2];
+  const int c0 = threadIdx.x % TPR * W;
   P w[NP];
   float acc[NP][W];
 #pragma unroll
   for (int j = 0; j < NP; ++j) {
-    const int c = c0 + j * TPB * W;
+    const int c = c0 + j * TPR * W;
 #pragma unroll
     for (int i = 0; i < W; ++i) {
       w[j][i] = (ET)1.f;
@@ -185,15 +213,17 @@ __global__ void __launch_bounds__(TPB) qmoe_rms_norm_grad(const NormGrad a, long
     if (a.w) w[j] = load_piece<ET, W>(static_cast<const ET*>(a.w) + c, a.H - c);
   }
   int turn = 0;
-  for (long m = blockIdx.x; m < a.M; m += gridDim.x, turn ^= 1) {
+  for (long m0 = (long)blockIdx.x * R; m0 < a.M; m0 += (long)gridDim.x * R, turn ^= 1) {
+    const long m = m0 + threadIdx.x / TPR;
+    const int H = m < a.M ? a.H : 0;
     P h[NP], g[NP], d[NP];
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
-      const int c = c0 + j * TPB * W;
-      h[j] = load_piece<ET, W>(static_cast<const ET*>(a.h) + m * a.H + c, a.H - c);
-      g[j] = load_piece<ET, W>(static_cast<const ET*>(a.dy) + m * a.H + c, a.H - c);
+      const int c = c0 + j * TPR * W;
+      h[j] = load_piece<ET, W>(static_cast<const ET*>(a.h) + m * a.H + c, H - c);
+      g[j] = load_piece<ET, W>(static_cast<const ET*>(a.dy) + m * a.H + c, H - c);
       d[j] = P{};
-      if (a.ds && a.dh) d[j] = load_piece<ET, W>(static_cast<const ET*>(a.ds) + m * a.H + c, a.H - c);
+      if (a.ds && a.dh) d[j] = load_piece<ET, W>(static_cast<const ET*>(a.ds) + m * a.H + c, H - c);
     }
     float v[2] = {0.f, 0.f};
 #pragma unroll
@@ -203,11 +233,11 @@ __global__ void __launch_bounds__(TPB) qmoe_rms_norm_grad(const NormGrad a, long
         v[0] = fmaf((float)h[j][i], (float)h[j][i], v[0]);
         v[1] = fmaf((float)g[j][i] * (float)w[j][i], (float)h[j][i], v[1]);
       }
-    block_sum<2, NW>(v, red, turn);
+    row_sum<2, TPR>(v, red, turn);
     const float s = 1.f / sqrtf(v[0] / (float)a.H + a.eps), mean = v[1] * s / (float)a.H;
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
-      const int c = c0 + j * TPB * W;
+      const int c = c0 + j * TPR * W;
       P o;
 #pragma unroll
       for (int i = 0; i < W; ++i) {
@@ -215,24 +245,39 @@ __global__ void __launch_bounds__(TPB) qmoe_rms_norm_grad(const NormGrad a, long
         o[i] = (ET)fmaf(s, gi * (float)w[j][i] - n * mean, (float)d[j][i]);
         acc[j][i] = fmaf(gi, n, acc[j][i]);
       }
-      if (a.dh) store_piece<ET, W>(static_cast<ET*>(a.dh) + m * a.H + c, a.H - c, o);
+      if (a.dh) store_piece<ET, W>(static_cast<ET*>(a.dh) + m * a.H + c, H - c, o);
     }
   }
   if (!a.dw) return;
+  if constexpr (R > 1) {
+    // a column's sums of the workgroup's R rows at a time, in their order
+    __shared__ float cols[R][TPR * W];
+#pragma unroll
+    for (int i = 0; i < W; ++i) cols[threadIdx.x / TPR][c0 + i] = acc[0][i];
+    __syncthreads();
+    for (int c = threadIdx.x; c < TPR * W && c < ldp; c += 256) {
+      float s = 0.f;
+#pragma unroll 8
+      for (int r = 0; r < R; ++r) s += cols[r][c];
+      a.partial[blockIdx.x * ldp + c] = s;
+    }
+    return;
+  }
 #pragma unroll
   for (int j = 0; j < NP; ++j)
 #pragma unroll
     for (int i = 0; i < W; i += 4) {
-      const int c = c0 + j * TPB * W + i;
+      const int c = c0 + j * TPR * W + i;
       if (c < ldp) *(f32x4*)(a.partial + blockIdx.x * ldp + c) = f32x4{acc[j][i], acc[j][i + 1], acc[j][i + 2], acc[j][i + 3]};
     }
 }
 
 // Rows too long for registers: read twice; 1 / root mean square of every row
-// into rstd for the weight's gradient.
+// into rstd for the weight's gradient, which reads them again.  1024 x 32768
+// bfloat16: 88 us for 268 MB.
 template <typename ET>
 __global__ void __launch_bounds__(1024) qmoe_rms_norm_grad_long(const NormGrad a, float* __restrict__ rstd) {
-  constexpr int W = 16 / (int)sizeof(ET), TPB = 1024;
+  constexpr int W = 16 / (int)sizeof(ET), TPR = 1024;
   using P = typename RowPiece<ET, W>::type;
   __shared__ float red[2][16][2];
   const ET* w = static_cast<const ET*>(a.w);
@@ -241,7 +286,7 @@ __global__ void __launch_bounds__(1024) qmoe_rms_norm_grad_long(const NormGrad a
     const ET* hp = static_cast<const ET*>(a.h) + m * a.H;
     const ET* gp = static_cast<const ET*>(a.dy) + m * a.H;
     float v[2] = {0.f, 0.f};
-    for (int c = threadIdx.x * W; c < a.H; c += TPB * W) {
+    for (int c = threadIdx.x * W; c < a.H; c += TPR * W) {
       const P h = load_piece<ET, W>(hp + c, a.H - c), g = load_piece<ET, W>(gp + c, a.H - c);
       P wp;
       if (w) wp = load_piece<ET, W>(w + c, a.H - c);
@@ -251,11 +296,11 @@ __global__ void __launch_bounds__(1024) qmoe_rms_norm_grad_long(const NormGrad a
         v[1] = fmaf((float)g[i] * (w ? (float)wp[i] : 1.f), (float)h[i], v[1]);
       }
     }
-    block_sum<2, 16>(v, red, turn);
+    row_sum<2, TPR>(v, red, turn);
     const float s = 1.f / sqrtf(v[0] / (float)a.H + a.eps), mean = v[1] * s / (float)a.H;
     if (a.dw && threadIdx.x == 0) rstd[m] = s;
     if (!a.dh) continue;
-    for (int c = threadIdx.x * W; c < a.H; c += TPB * W) {
+    for (int c = threadIdx.x * W; c < a.H; c += TPR * W) {
       const int n = a.H - c;
       const P h = load_piece<ET, W>(hp + c, n), g = load_piece<ET, W>(gp + c, n);
       P wp, d = {}, o;
@@ -290,70 +335,97 @@ __global__ void __launch_bounds__(256) qmoe_norm_weight_grad(const NormGrad a, c
     if (c + i < ldp) *(f32x4*)(partial + blockIdx.y * ldp + c + i) = f32x4{acc[i], acc[i + 1], acc[i + 2], acc[i + 3]};
 }
 
-// dw = sum of B rows of partial sums: 64 columns a workgroup, four a thread,
-// sixteen threads over the rows of each (in a fixed order).
+// dw = sum of B rows of partial sums: 32 columns a workgroup, four a thread,
+// thirty-two threads over the rows of each (in a fixed order).
 template <typename ET>
 __global__ void __launch_bounds__(256) qmoe_norm_sum(const float* __restrict__ partial, long ldp, int B, int H,
                                                      ET* __restrict__ dw) {
-  __shared__ f32x4 red[16][16];
-  const int q = threadIdx.x & 15, g = threadIdx.x >> 4;
-  const int c = (blockIdx.x * 16 + q) * 4;
+  __shared__ f32x4 red[32][8];
+  const int q = threadIdx.x & 7, g = threadIdx.x >> 3;
+  const int c = (blockIdx.x * 8 + q) * 4;
   f32x4 s = {0.f, 0.f, 0.f, 0.f};
   if (c < ldp) {
 #pragma unroll 8
-    for (int b = g; b < B; b += 16) s += *(const f32x4*)(partial + b * ldp + c);
+    for (int b = g; b < B; b += 32) s += *(const f32x4*)(partial + b * ldp + c);
   }
   red[g][q] = s;
   __syncthreads();
-  if (g > 0) return;
+  if (threadIdx.x >= 32) return;
+  const int k = threadIdx.x;  // a column a thread
+  float t = 0.f;
 #pragma unroll
-  for (int k = 1; k < 16; ++k) s += red[k][q];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (c + i < H) dw[c + i] = (ET)s[i];
+  for (int r = 0; r < 32; ++r) t += red[r][k >> 2][k & 3];
+  if (blockIdx.x * 32 + k < H) dw[blockIdx.x * 32 + k] = (ET)t;
 }
 
 constexpr int kCUs = 256;
 constexpr int kLongRows = 256;  // rows of partial sums for rows too long for registers
 
 // Threads a row and pieces a thread; 0 pieces: too long for registers.
+// Few rows: a piece a thread, up to 1024 (16 x 4096 bfloat16 2.9 and in 8 bits 3.4
+// us, with 256 x 2 3.2 and 3.9, with 64 x 8 5.6 and 7.9); many: 256 threads where
+// the row allows (8192 x 4096 48 and 57 us, 128 x 4 48 and 60, 1024 x 1 49 and 72).
 struct NormShape {
   int threads, np;
 };
-NormShape norm_shape(long pieces) {
+NormShape norm_shape(long M, long pieces, long most) {
+  if (pieces <= 8) return {8, 1};
+  if (pieces <= 16) return {16, 1};
+  if (pieces <= 32) return {32, 1};
   if (pieces <= 64) return {64, 1};
-  if (pieces <= 128) return {64, 2};
+  if (pieces <= 128) return {128, 1};
   if (pieces <= 256) return {256, 1};
+  if (M <= 2 * kCUs && pieces <= 512) return {512, 1};
+  if (M <= 2 * kCUs && pieces <= 1024) return {1024, 1};
   if (pieces <= 512) return {256, 2};
   if (pieces <= 1024) return {256, 4};
-  if (pieces <= 2048) return {1024, 2};
-  if (pieces <= 4096) return {1024, 4};
+  if (pieces <= 2048) return {512, 4};
+  if (pieces <= most) return {512, 8};
   return {1024, 0};
 }
-unsigned norm_grid(long M, int threads) { return (unsigned)std::min<long>(M, kCUs * (2048 / threads)); }
-// (fewer in the backward pass: each leaves a row of partial sums)
-unsigned norm_grad_grid(long M, int threads) { return (unsigned)std::min<long>(M, kCUs * std::max(1, 512 / threads)); }
+unsigned norm_grid(long M, const NormShape& s) {
+  const long rows = rows_of(s.threads);
+  return (unsigned)std::min<long>((M + rows - 1) / rows, kCUs * (2048 / threads_of(s.threads)));
+}
+// Fewer in the backward pass, each of which leaves a row of partial sums: 8192 x
+// 4096 (256 x 2) 44 us on two a compute unit, 47 on four, 64 on one; 8192 x 2048
+// (256 x 1) 28 us on four, 32 on two; 8192 x 1024 (128 x 1) 20 us on four, 22 on
+// eight, 24 on two.
+unsigned norm_grad_grid(long M, const NormShape& s) {
+  const long rows = rows_of(s.threads);
+  const long per = s.threads <= 256 && s.np == 1 ? 4 : s.threads <= 256 ? 2 : 1;
+  return (unsigned)std::min<long>((M + rows - 1) / rows, kCUs * per);
+}
+// The longest rows (in pieces) that stay in registers: in the backward pass 16-bit
+// rows of 512 threads x 8 pieces would spill 900 bytes a lane (1024 x 32768: 254 us).
+template <typename ET>
+constexpr long kMostGrad = sizeof(ET) == 4 ? 4096 : 2048;
 
-// f(TPB, NP) with both as compile-time constants.
+// f(TPR, NP) with both as compile-time constants.
 template <typename G>
 void with_shape(const NormShape& s, G f) {
 #define QMOE_SHAPE(T, N) \
   if (s.threads == T && s.np == N) return f(std::integral_constant<int, T>{}, std::integral_constant<int, N>{});
+  QMOE_SHAPE(8, 1)
+  QMOE_SHAPE(16, 1)
+  QMOE_SHAPE(32, 1)
   QMOE_SHAPE(64, 1)
-  QMOE_SHAPE(64, 2)
+  QMOE_SHAPE(128, 1)
   QMOE_SHAPE(256, 1)
+  QMOE_SHAPE(512, 1)
+  QMOE_SHAPE(1024, 1)
   QMOE_SHAPE(256, 2)
   QMOE_SHAPE(256, 4)
-  QMOE_SHAPE(1024, 2)
-  QMOE_SHAPE(1024, 4)
+  QMOE_SHAPE(512, 4)
+  QMOE_SHAPE(512, 8)
 #undef QMOE_SHAPE
 }
 
 template <typename ET, int F>
 hipError_t norm_t(const Norm& a, hipStream_t st) {
   constexpr int W = 16 / (int)sizeof(ET);
-  const NormShape s = norm_shape((a.H + W - 1) / W);
-  const dim3 grid(norm_grid(a.M, s.threads)), block(s.threads);
+  const NormShape s = norm_shape(a.M, (a.H + W - 1) / W, 4096);
+  const dim3 grid(norm_grid(a.M, s)), block(threads_of(s.threads));
   if (s.np == 0) {
     hipLaunchKernelGGL((qmoe_rms_norm_long<ET, F>), grid, block, 0, st, a);
   } else {
@@ -376,12 +448,12 @@ long padded(long H) { return (H + 3) / 4 * 4; }
 template <typename ET>
 hipError_t norm_grad_t(const NormGrad& a, hipStream_t st) {
   constexpr int W = 16 / (int)sizeof(ET);
-  const NormShape s = norm_shape((a.H + W - 1) / W);
+  const NormShape s = norm_shape(a.M, (a.H + W - 1) / W, kMostGrad<ET>);
   const long ldp = padded(a.H);
   const float* partial = a.partial;
   unsigned rows = 0;
   if (a.M > 0) {
-    rows = norm_grad_grid(a.M, s.threads);
+    rows = norm_grad_grid(a.M, s);
     if (s.np == 0) {
       float* rstd = a.partial + kLongRows * ldp;
       hipLaunchKernelGGL(qmoe_rms_norm_grad_long<ET>, dim3(rows), dim3(1024), 0, st, a, rstd);
@@ -390,11 +462,13 @@ hipError_t norm_grad_t(const NormGrad& a, hipStream_t st) {
         hipLaunchKernelGGL(qmoe_norm_weight_grad<ET>, dim3((unsigned)((a.H + 256 * W - 1) / (256 * W)), rows), dim3(256), 0, st, a, rstd, a.partial, ldp);
     } else {
       with_shape(s, [&](auto t, auto n) {
-        hipLaunchKernelGGL((qmoe_rms_norm_grad<ET, decltype(n)::value, decltype(t)::value>), dim3(rows), dim3(s.threads), 0, st, a, ldp);
+        constexpr int T = decltype(t)::value, N = decltype(n)::value;
+        if constexpr (T * N <= kMostGrad<ET>)
+          hipLaunchKernelGGL((qmoe_rms_norm_grad<ET, N, T>), dim3(rows), dim3(threads_of(s.threads)), 0, st, a, ldp);
       });
     }
   }
-  if (a.dw) hipLaunchKernelGGL(qmoe_norm_sum<ET>, dim3((unsigned)((a.H + 63) / 64)), dim3(256), 0, st, partial, ldp, (int)rows, a.H, (ET*)a.dw);
+  if (a.dw) hipLaunchKernelGGL(qmoe_norm_sum<ET>, dim3((unsigned)((a.H + 31) / 32)), dim3(256), 0, st, partial, ldp, (int)rows, a.H, (ET*)a.dw);
   return hipGetLastError();
 }
 
@@ -409,9 +483,9 @@ hipError_t launch_rms_norm(int type, const Norm& a, hipStream_t st) {
 size_t norm_partials(int type, long M, long H) {
   if (M == 0) return 0;
   const long W = type == ROW_F32 ? 4 : 8;
-  const NormShape s = norm_shape((H + W - 1) / W);
+  const NormShape s = norm_shape(M, (H + W - 1) / W, type == ROW_F32 ? kMostGrad<float> : kMostGrad<_Float16>);
   if (s.np == 0) return (size_t)(kLongRows * padded(H) + M);
-  return (size_t)norm_grad_grid(M, s.threads) * (size_t)padded(H);
+  return (size_t)norm_grad_grid(M, s) * (size_t)padded(H);
 }
 
 hipError_t launch_rms_norm_grad(int type, const NormGrad& a, hipStream_t st) {

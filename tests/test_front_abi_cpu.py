@@ -99,7 +99,7 @@ def _norm_back(lib, g=T(F32, 6, 40), ds=T(F32, 6, 40), x=T(F32, 6, 40), w=T(F32,
     (dict(g=None), NULL), (dict(x=None), NULL), (dict(w=None), NULL), (dict(g=T(F16, 6, 40)), DTYPE),
     (dict(ds=T(F16, 6, 40)), DTYPE), (dict(gi=T(F16, 6, 40)), DTYPE), (dict(gw=T(F16, 40)), DTYPE), (dict(w=T(F16, 40)), DTYPE),
     (dict(ds=T(F32, 6, 41)), SHAPE), (dict(gi=T(F32, 7, 40)), SHAPE), (dict(gw=T(F32, 39)), SHAPE), (dict(gw=T(F32, 1, 40)), SHAPE),
-    (dict(eps=0.0), ATTR), (dict(ws=None), NULL), (dict(n=6 * 40 * 4 - 1), WORKSPACE), (dict(ws=GOOD + 16), ALIGN),
+    (dict(eps=0.0), ATTR), (dict(ws=None), NULL), (dict(n=40 * 4 - 1), WORKSPACE), (dict(ws=GOOD + 16), ALIGN),
     (dict(gi=T(F32, 6, 40, ptr=None)), NULL), (dict(g=T(F32, 6, 40, ptr=GOOD + 2)), ALIGN)])
 def test_norm_backward_refusals(lib, kw, want):
     assert _norm_back(lib, **kw) == want
@@ -109,7 +109,8 @@ def test_norm_workspace(lib):
     x, w = np.zeros((3, 10), np.float16), np.zeros(10, np.float16)
     size = lambda x, w, gw: qm.qmoe_rms_norm_backward_workspace_size(x, None, x, w, 1e-6, x, gw)  # noqa: E731
     assert size(x, w, None) == 0 and size(x[:0], w, w) == 0
-    assert size(x, w, w) == 3 * 12 * 4  # a row of sums a row of the norm, whole fours of columns
+    assert size(x, w, w) == 12 * 4  # one row of sums of a workgroup's rows, whole fours of columns
+    assert size(np.broadcast_to(x[:1], (33, 10)), w, w) == 2 * 12 * 4
     big = np.broadcast_to(x[:1, :1], (1 << 20, 4096))
     assert 0 < size(big, np.broadcast_to(w[:1], (4096,)), np.broadcast_to(w[:1], (4096,))) <= 1 << 25
 

@@ -96,6 +96,26 @@ def test_many_rows(torch, dt):
     check(torch, dt, 700, 520)
 
 
+@pytest.mark.parametrize("dt,M,H", [("float32", 33000, 24), ("bfloat16", 4200, 513), ("float16", 1100, 1500), ("bfloat16", 530, 4096),
+                                    ("float16", 260, 9000)])
+def test_more_rows_than_one_round_of_workgroups(torch, dt, M, H):
+    check(torch, dt, M, H)
+
+
+@pytest.mark.parametrize("M,H", [(70000, 64), (9000, 700), (4133, 4096), (3000, 8192), (1100, 20000)])
+def test_rows_do_not_depend_on_their_place(torch, M, H):
+    g = torch.Generator(device="cuda").manual_seed(H)
+    x, r, w = (torch.randn(*s, generator=g, device="cuda").bfloat16() for s in ((M, H), (M, H), (H,)))
+    whole = qm.rms_norm(x, w, r, format="int8", block_size=64)
+    gx, _ = qm.rms_norm_backward(r, x, w, r)
+    half = (M + 1) // 2  # (more than 512 rows: the same threads a row)
+    for lo, hi in ((0, half), (half, M)):
+        part = qm.rms_norm(x[lo:hi], w, r[lo:hi], format="int8", block_size=64)
+        for a, b in zip(whole, part):
+            assert torch.equal(a[lo:hi].view(torch.uint8), b.view(torch.uint8))
+        assert torch.equal(gx[lo:hi], qm.rms_norm_backward(r[lo:hi], x[lo:hi], w, r[lo:hi])[0])
+
+
 @pytest.mark.parametrize("scale,eps", [(1e-4, 1e-6), (100.0, 1e-5), (1e-3, 1e-12), (1.0, 10.0)])
 def test_magnitudes(torch, scale, eps):
     check(torch, "float16" if scale > 1e-3 else "bfloat16", 4, 96, scale=scale, eps=eps)
