@@ -18,23 +18,43 @@ __device__ __forceinline__ int key_of(float v) {
 __device__ __forceinline__ float of_key(int k) { return __int_as_float(k ^ ((k >> 31) & 0x7fffffff)); }
 constexpr int kNone = (int)0x807fffff;  // -infinity
 
-// x[j] <- e^x[j] for x <= 0 in 64 bits, within 2^-50 of itself (the series to r^12
-// over |r| <= ln 2 / 2); below -110, where float32 has only 0, it stays at e^-110.
+// Register j of a lane holds element lane + 64 j of a row of E; `none` past its end.
+template <int V>
+__device__ __forceinline__ void load_row(const float* __restrict__ row, int E, int lane, float none, float (&v)[V]) {
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int e = lane + 64 * j;
+    v[j] = row[min(e, E - 1)];  // (no branch: the loads go out together)
+  }
+#pragma unroll
+  for (int j = 0; j < V; ++j) v[j] = lane + 64 * j < E ? v[j] : none;
+}
+// A row's logits: +infinity counts as the largest float, -infinity and NaN
+// (masked) come back as -infinity.
+template <int V>
+__device__ __forceinline__ void load_logits(const float* __restrict__ row, int E, int lane, float (&v)[V]) {
+  load_row<V>(row, E, lane, -INFINITY, v);
+#pragma unroll
+  for (int j = 0; j < V; ++j) v[j] = fminf(fmaxf(v[j], -INFINITY), 3.4028234664e38f);  // (the larger of NaN and a number is the number)
+}
+
+// x[j] <- e^x[j] for x in [-110, 0] in 64 bits, within 2^-50 of itself (the
+// polynomial of degree 10 through e^r at the Chebyshev points of |r| <= ln 2 / 2).
 template <int V>
 __device__ __forceinline__ void exp_below(double (&x)[V]) {
-  constexpr double c[] = {1.0 / 39916800.0, 1.0 / 3628800.0, 1.0 / 362880.0, 1.0 / 40320.0, 1.0 / 5040.0, 1.0 / 720.0,
-                          1.0 / 120.0,      1.0 / 24.0,      1.0 / 6.0,      0.5,           1.0,          1.0};
+  constexpr double c[] = {2.764019739169484e-06, 2.480150431378554e-05, 0.00019841170230570286, 0.001388888893251478,
+                          0.008333333385699212,  0.041666666666573066,  0.16666666666554314,    0.5000000000000006,
+                          1.0000000000000067,    1.0};
   double n[V], p[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    x[j] = x[j] < -110.0 ? -110.0 : x[j];
     n[j] = __builtin_rint(x[j] * 1.4426950408889634);
     x[j] = fma(n[j], -0.6931471805599453, x[j]);
     x[j] = fma(n[j], -2.3190468138462996e-17, x[j]);
-    p[j] = 1.0 / 479001600.0;
+    p[j] = 2.762637106569636e-07;
   }
 #pragma unroll
-  for (int i = 0; i < 12; ++i)
+  for (int i = 0; i < 10; ++i)
 #pragma unroll
     for (int j = 0; j < V; ++j) p[j] = fma(p[j], x[j], c[i]);
 #pragma unroll
@@ -47,43 +67,34 @@ __device__ __forceinline__ double reciprocal(double d) {
   return fma(y, fma(-d, y, 1.0), y);
 }
 
-// A row's logits, lane + 64 j: +infinity counts as the largest float, -infinity
-// and NaN (masked) come back as -infinity.
-template <int V>
-__device__ __forceinline__ void load_logits(const float* __restrict__ row, int E, int lane, float (&v)[V]) {
-#pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const float x = lane + 64 * j < E ? row[lane + 64 * j] : -INFINITY;
-    v[j] = x != x ? -INFINITY : fminf(x, 3.4028234664e38f);
-  }
-}
-
 // One wavefront per token, expert lane + 64 j in register j.  The scores are
 // evaluated in 64 bits and rounded once to float32: an expert is selected by
 // comparing its score plus bias with others', and two that differ in float32's
 // last bits would change places with the rounding errors of a float32 exponential.
 //
-// Bound by the vector instructions: reductions stay in registers, ranks of groups
+// Bound by the vector instructions (524 a wavefront below, 83 % of the time, a fifth
+// of them the 64-bit exponentials): reductions stay in registers, ranks of groups
 // are counted by all lanes, and a round of the selection is one reduction, a compare
 // a register (whose ballots give the lowest expert that holds the largest key) and
-// a write to one lane.  16384 x 256 logits, 6 of 16 groups' 5, softmax: FIGURES
+// a write to one lane.  16384 x 256 logits, 6 out of 5 of 16 groups, softmax: 17.7
+// us (30.5 with reductions and scores through LDS and library exponentials) where
+// its bytes take 3.5; 16 x 128, sigmoid: 3.9 us.
 // k <= 64 (else MANY: pick r in lane r % 64 of register r / 64).
 template <int V, bool MANY>
 __global__ void __launch_bounds__(256) qmoe_route_scored(const float* __restrict__ logits,
                                                          const float* __restrict__ bias, int T, RouteScored a, int b0,
                                                          int* __restrict__ idx, float* __restrict__ w) {
   __shared__ float lds[4][64 * V];
-  const int wave = threadIdx.x >> 6, lane = lane_id();
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = lane_id();
   const int t = (b0 + blockIdx.x) * 4 + wave;
   if (t >= T) return;
-  float v[V], p[V], b[V];
+  float v[V], p[V], b[V] = {};
   load_logits<V>(logits + (long)t * a.E, a.E, lane, v);
-#pragma unroll
-  for (int j = 0; j < V; ++j) b[j] = bias && lane + 64 * j < a.E ? bias[lane + 64 * j] : 0.f;
+  if (bias) load_row<V>(bias, a.E, lane, 0.f, b);
   double e[V];
   if (a.sigmoid) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) e[j] = -fabs((double)v[j]);
+    for (int j = 0; j < V; ++j) e[j] = (double)fmaxf(-fabsf(v[j]), -110.f);  // (e^-110 is 0 in float32)
     exp_below<V>(e);
 #pragma unroll
     for (int j = 0; j < V; ++j) p[j] = (float)((v[j] < 0.f ? e[j] : 1.0) * reciprocal(1.0 + e[j]));
@@ -92,17 +103,14 @@ __global__ void __launch_bounds__(256) qmoe_route_scored(const float* __restrict
 #pragma unroll
     for (int j = 1; j < V; ++j) m = max(m, key_of(v[j]));
     // (a row that is all masked: nothing is selected, whatever the scores are)
-    const double top = (double)fmaxf(of_key(wave_max_int(m)), -3.4028234664e38f);
+    const float top = fmaxf(of_key(wave_max_int(m)), -3.4028234664e38f);
+    // (e^-110 is 0 in float32, and what masked experts add to a sum of at least 1 stays below 64 bits)
 #pragma unroll
-    for (int j = 0; j < V; ++j) e[j] = (double)v[j] - top;
+    for (int j = 0; j < V; ++j) e[j] = fmax((double)v[j] - (double)top, -110.0);
     exp_below<V>(e);
     double sum = 0.0;
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      e[j] = v[j] == -INFINITY ? 0.0 : e[j];
-      sum += e[j];
-    }
-    // (the largest one's e is 1)
+    for (int j = 0; j < V; ++j) sum += e[j];
     const double inv = reciprocal(fmax(wave_sum_double(sum), 1.0));
 #pragma unroll
     for (int j = 0; j < V; ++j) p[j] = (float)(e[j] * inv);
@@ -110,8 +118,8 @@ __global__ void __launch_bounds__(256) qmoe_route_scored(const float* __restrict
   int c[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    const float x = p[j] + b[j];
-    c[j] = v[j] == -INFINITY || x != x ? kNone : key_of(x);
+    const float x = p[j] + fmaxf(b[j], -INFINITY);  // (a bias of NaN as -infinity)
+    c[j] = v[j] == -INFINITY ? kNone : key_of(x);
   }
   if (a.kept < a.groups) {
     int* s = reinterpret_cast<int*>(lds[wave]);
@@ -226,7 +234,7 @@ __global__ void __launch_bounds__(256) qmoe_route_scored_grad(const float* __res
                                                               const void* __restrict__ idx, bool idx64, int T,
                                                               RouteScored a, int b0, float* __restrict__ gl) {
   extern __shared__ char smem[];  // per wavefront: k experts, k values
-  const int wave = threadIdx.x >> 6, lane = lane_id();
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = lane_id();
   int* se = reinterpret_cast<int*>(smem) + wave * 2 * a.k;
   float* sv = reinterpret_cast<float*>(se + a.k);
   const int t = (b0 + blockIdx.x) * 4 + wave;
