@@ -38,6 +38,7 @@ struct LinearGemm {
   void* out;         // [M][No], dx [M][K] or dw [G][N][K]
   float* partial;    // splits > 1: [splits][rows of out][cols4] fp32 sums
   int splits;        // ranges of r
+  int stream;        // what is written passes the L2 caches' size: stored past them
   LinearAct act;
 };
 

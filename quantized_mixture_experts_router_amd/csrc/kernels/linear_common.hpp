@@ -239,6 +239,24 @@ __device__ __forceinline__ void store_w(ET* p, int n, const float (&v)[W]) {
   }
 }
 
+// A product's output: past the caches where it exceeds them all the same
+// (`stream`; uniform), so that the operands stay there.
+template <typename ET, int W, bool VEC>
+__device__ __forceinline__ void put_w(ET* p, int n, const float (&v)[W], int stream) {
+  if constexpr (VEC) {
+    if (stream) {
+      typename LinVec<ET, W>::type t;
+#pragma unroll
+      for (int i = 0; i < W; ++i) t[i] = (ET)v[i];
+      asm volatile("");  // (the compiler would make one plain store of both branches')
+      __builtin_nontemporal_store(t, (typename LinVec<ET, W>::type*)p);
+      asm volatile("");
+      return;
+    }
+  }
+  store_w<ET, W, VEC>(p, n, v);
+}
+
 // The epilogue of W consecutive columns c .. of R output rows m[r] (those with
 // ok[r]), the columns' biases in b: z = the float32 sums + bias,
 // pre-activation out, activation, residual, one rounding to the type.  VEC: a
@@ -257,7 +275,7 @@ __device__ __forceinline__ void linear_rows(const LinearGemm& g, float (&z)[R][W
     ET* pre = static_cast<ET*>(g.pre) + c;
 #pragma unroll
     for (int r = 0; r < R; ++r)
-      if (ok[r]) store_w<ET, W, VEC>(pre + (long)m[r] * g.N, n, z[r]);
+      if (ok[r]) put_w<ET, W, VEC>(pre + (long)m[r] * g.N, n, z[r], g.stream);
   }
   if constexpr (ACT == kActSwiglu) {
     constexpr int H = W / 2;
@@ -281,7 +299,7 @@ __device__ __forceinline__ void linear_rows(const LinearGemm& g, float (&z)[R][W
     ET* out = static_cast<ET*>(g.out) + (c >> 1);
 #pragma unroll
     for (int r = 0; r < R; ++r)
-      if (ok[r]) store_w<ET, H, VEC>(out + m[r] * No, n >> 1, y[r]);
+      if (ok[r]) put_w<ET, H, VEC>(out + m[r] * No, n >> 1, y[r], g.stream);
   } else {
 #pragma unroll
     for (int r = 0; r < R; ++r)
@@ -301,7 +319,7 @@ __device__ __forceinline__ void linear_rows(const LinearGemm& g, float (&z)[R][W
     ET* out = static_cast<ET*>(g.out) + c;
 #pragma unroll
     for (int r = 0; r < R; ++r)
-      if (ok[r]) store_w<ET, W, VEC>(out + (long)m[r] * g.N, n, z[r]);
+      if (ok[r]) put_w<ET, W, VEC>(out + (long)m[r] * g.N, n, z[r], g.stream);
   }
 }
 
@@ -337,7 +355,7 @@ __device__ __forceinline__ void linear_rows8(const LinearGemm& g, const float (&
 // 16-byte pieces in the order i ^ swz (b lies in that order too), so that lanes
 // 256 bytes apart meet different banks.
 __device__ __forceinline__ void linear_codes16(const Rows8& q, int N, const char* sums, const f32x4 (&b)[4], int swz,
-                                               int c, long m, bool ok) {
+                                               int c, long m, bool ok, int stream) {
   f32x4 v[4];
   uint32_t top = 0;
 #pragma unroll
@@ -361,7 +379,8 @@ __device__ __forceinline__ void linear_codes16(const Rows8& q, int N, const char
   if (swz & 2) u = u32x4{u[2], u[3], u[0], u[1]};
   const int n = N - c;
   if (!ok || n <= 0) return;
-  store_piece<uint8_t, 16>(q.codes + m * N + c, n, __builtin_bit_cast(RowPiece<uint8_t, 16>::type, u));
+  const auto t = __builtin_bit_cast(RowPiece<uint8_t, 16>::type, u);
+  store_piece<uint8_t, 16>(q.codes + m * N + c, n, t, stream);
   if ((c & ((1 << bl) - 1)) == 0) q.scales[m * ((N + (1 << bl) - 1) >> bl) + (c >> bl)] = __uint_as_float(s);
 }
 

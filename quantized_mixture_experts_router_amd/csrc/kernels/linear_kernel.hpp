@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(64 * WQ * WP) qmoe_linear(const LinearGemm g, 
       for (int s0 = 0; s0 < WQ * 32; s0 += R16) {
         const int sr = s0 + r16;
         const int qr = (sr >> 5) * (TQ * 16) + b2 * 32 + (sr & 31);
-        linear_codes16(g.pre8, g.N, so + sr * SST + c16 * 4, bias16, swz, p0 + c16, (long)q0 + qr, qr < qrows);
+        linear_codes16(g.pre8, g.N, so + sr * SST + c16 * 4, bias16, swz, p0 + c16, (long)q0 + qr, qr < qrows, g.stream);
       }
     }
     if (!inside) continue;
@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(64 * WQ * WP) qmoe_linear(const LinearGemm g, 
           ET* out = static_cast<ET*>(g.out) + (MODE == LIN_DW ? (long)grp * g.N * g.K : 0) + c;
 #pragma unroll
           for (int r = 0; r < RS; ++r)
-            if (ok[r]) store_w<ET, W, VEC>(out + (long)m[r] * g.K, g.K - c, z[r]);
+            if (ok[r]) put_w<ET, W, VEC>(out + (long)m[r] * g.K, g.K - c, z[r], g.stream);
         }
       }
     };

@@ -19,6 +19,7 @@ struct Norm {
   Rows8 q;        // codes NULL: none
   long M;
   int H;
+  int stream;     // outputs past the caches (set by the launch)
   float eps;
 };
 hipError_t launch_rms_norm(int type, const Norm& a, hipStream_t st);
@@ -34,6 +35,7 @@ struct NormGrad {
   float* partial;  // norm_partials floats (dw)
   long M;
   int H;
+  int stream;      // as above
   float eps;
 };
 // Floats of partial.

@@ -3,6 +3,7 @@
 // between its sum of squares and its output.
 #include <algorithm>
 
+#include "launches.h"
 #include "norm.h"
 #include "rows8.hpp"
 #include "tokens.h"
@@ -39,10 +40,13 @@ constexpr int threads_of(int TPR) { return TPR < 256 ? 256 : TPR; }
 // Sums of N values over the TPR threads of a row, the same bits in every one;
 // red: [2][wavefronts][N] for rows of several wavefronts, where the caller
 // alternates turn (one barrier a call).
-template <int N, int TPR>
-__device__ __forceinline__ void row_sum(float (&v)[N], float (*red)[threads_of(TPR) / 64][N], int turn) {
+template <typename S, int N, int TPR>
+__device__ __forceinline__ void row_sum(S (&v)[N], S (*red)[threads_of(TPR) / 64][N], int turn) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = lanes_sum<TPR < 64 ? TPR : 64>(v[i]);
+  for (int i = 0; i < N; ++i) {
+    if constexpr (std::is_same<S, double>::value) v[i] = wave_sum_double<TPR < 64 ? TPR : 64>(v[i]);
+    else v[i] = lanes_sum<TPR < 64 ? TPR : 64>(v[i]);
+  }
   if constexpr (TPR > 64) {
     if (lane_id() == 0) {
 #pragma unroll
@@ -57,6 +61,32 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float (*red)[threads_of(T
       for (int k = 1; k < TPR / 64; ++k) v[i] += red[turn][first + k][i];
     }
   }
+}
+
+// 1 / sqrt(ss / H + eps) as the sum of two floats.  A value goes to 8 bits by
+// the side of a border that it lies on, and each float32 rounding before puts a
+// few in a million on the other: the threads' float32 sums are added in 64 bits, s
+// keeps its tail, and h s w is rounded once (forward only; next to HBM this is
+// free).  Squares that pass float32 leave 0.
+struct RowScale {
+  float hi, lo;
+};
+__device__ __forceinline__ RowScale row_scale(double ss, int H, float eps) {
+  const double x = ss / (double)H + (double)eps;
+  // the hardware's estimate (2^-22 at least) and a step of Newton's method
+  double y = __builtin_amdgcn_rsq(x);
+  y = fma(y * 0.5, fma(-x * y, y, 1.0), y);
+  y = x > 1e300 ? 0.0 : y;
+  const float hi = (float)y;
+  return {hi, (float)(y - (double)hi)};
+}
+// h s w; EXACT: h w is (16-bit types), else its error goes along.
+template <bool EXACT>
+__device__ __forceinline__ float scaled(float h, float w, const RowScale& s) {
+  const float p = h * w;
+  float low = p * s.lo;
+  if constexpr (!EXACT) low = fmaf(fmaf(h, w, -p), s.hi, low);
+  return fmaf(p, s.hi, low);
 }
 
 // h of a piece: x + r in float32, rounded to the type (it is what the residual
@@ -76,7 +106,7 @@ __device__ __forceinline__ void put_piece(const Norm& a, long m, int c, const fl
     typename RowPiece<ET, W>::type o;
 #pragma unroll
     for (int i = 0; i < W; ++i) o[i] = (ET)y[i];
-    store_piece<ET, W>(static_cast<ET*>(a.y) + m * a.H + c, n, o);
+    store_piece<ET, W>(static_cast<ET*>(a.y) + m * a.H + c, n, o, a.stream);
   }
   if constexpr (F >= 0) {
     const int bl = a.q.block_log;
@@ -85,7 +115,7 @@ __device__ __forceinline__ void put_piece(const Norm& a, long m, int c, const fl
     for (int i = 0; i < W; ++i) top = max(top, abs_bits(y[i]));
     const uint32_t s = r8_scale_bits<F>(lanes_max(top, min(bl - (W == 8 ? 3 : 2), lanes)));
     if (n > 0) {
-      store_codes<F, W>(a.q.codes + m * a.H + c, n, y, r8_inverse(s));
+      store_codes<F, W>(a.q.codes + m * a.H + c, n, y, r8_inverse(s), a.stream);
       if ((c & ((1 << bl) - 1)) == 0) a.q.scales[m * ((a.H + (1 << bl) - 1) >> bl) + (c >> bl)] = __uint_as_float(s);
     }
   }
@@ -100,7 +130,7 @@ __global__ void __launch_bounds__(threads_of(TPR)) qmoe_rms_norm(const Norm a) {
   constexpr int W = 16 / (int)sizeof(ET), R = rows_of(TPR);
   constexpr int kLanes = TPR >= 64 ? 6 : TPR == 32 ? 5 : TPR == 16 ? 4 : 3;
   using P = typename RowPiece<ET, W>::type;
-  __shared__ float red[2][threads_of(TPR) / 64][1];
+  __shared__ double red[2][threads_of(TPR) / 64][1];
   const int c0 = threadIdx.x % TPR * W;
   P w[NP];
 #pragma unroll
@@ -131,21 +161,22 @@ __global__ void __launch_bounds__(threads_of(TPR)) qmoe_rms_norm(const Norm a) {
       for (int j = 0; j < NP; ++j) {
         const int c = c0 + j * TPR * W;
         add_piece<ET, W>(h[j], r[j]);
-        if (a.sum) store_piece<ET, W>(static_cast<ET*>(a.sum) + m * a.H + c, H - c, h[j]);
+        if (a.sum) store_piece<ET, W>(static_cast<ET*>(a.sum) + m * a.H + c, H - c, h[j], a.stream);
       }
     }
-    float ss[1] = {0.f};
+    float sq = 0.f;
 #pragma unroll
     for (int j = 0; j < NP; ++j)
 #pragma unroll
-      for (int i = 0; i < W; ++i) ss[0] = fmaf((float)h[j][i], (float)h[j][i], ss[0]);
-    row_sum<1, TPR>(ss, red, turn);
-    const float s = 1.f / sqrtf(ss[0] / (float)a.H + a.eps);
+      for (int i = 0; i < W; ++i) sq = fmaf((float)h[j][i], (float)h[j][i], sq);
+    double ss[1] = {sq};
+    row_sum<double, 1, TPR>(ss, red, turn);
+    const RowScale s = row_scale(ss[0], a.H, a.eps);
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
       float y[W];
 #pragma unroll
-      for (int i = 0; i < W; ++i) y[i] = (float)h[j][i] * s * (float)w[j][i];
+      for (int i = 0; i < W; ++i) y[i] = scaled<sizeof(ET) == 2>((float)h[j][i], (float)w[j][i], s);
       put_piece<ET, F, W>(a, m, c0 + j * TPR * W, y, kLanes);
     }
   }
@@ -156,7 +187,7 @@ template <typename ET, int F>
 __global__ void __launch_bounds__(1024) qmoe_rms_norm_long(const Norm a) {
   constexpr int W = 16 / (int)sizeof(ET), TPR = 1024;
   using P = typename RowPiece<ET, W>::type;
-  __shared__ float red[2][16][1];
+  __shared__ double red[2][16][1];
   const int c0 = threadIdx.x * W;
   auto piece = [&](long m, int c) {
     P h = load_piece<ET, W>(static_cast<const ET*>(a.x) + m * a.H + c, a.H - c);
@@ -165,15 +196,17 @@ __global__ void __launch_bounds__(1024) qmoe_rms_norm_long(const Norm a) {
   };
   int turn = 0;
   for (long m = blockIdx.x; m < a.M; m += gridDim.x, turn ^= 1) {
-    float ss[1] = {0.f};
+    double ss[1] = {0.0};
     for (int c = c0; c < a.H; c += TPR * W) {
       const P h = piece(m, c);
-      if (a.sum && a.r) store_piece<ET, W>(static_cast<ET*>(a.sum) + m * a.H + c, a.H - c, h);
+      if (a.sum && a.r) store_piece<ET, W>(static_cast<ET*>(a.sum) + m * a.H + c, a.H - c, h, a.stream);
+      float sq = 0.f;
 #pragma unroll
-      for (int i = 0; i < W; ++i) ss[0] = fmaf((float)h[i], (float)h[i], ss[0]);
+      for (int i = 0; i < W; ++i) sq = fmaf((float)h[i], (float)h[i], sq);
+      ss[0] += (double)sq;
     }
-    row_sum<1, TPR>(ss, red, turn);
-    const float s = 1.f / sqrtf(ss[0] / (float)a.H + a.eps);
+    row_sum<double, 1, TPR>(ss, red, turn);
+    const RowScale s = row_scale(ss[0], a.H, a.eps);
     // (every lane of a wavefront takes part in its blocks' largest magnitude)
     for (int base = 0; base < a.H; base += TPR * W) {
       const int c = base + c0;
@@ -183,7 +216,7 @@ __global__ void __launch_bounds__(1024) qmoe_rms_norm_long(const Norm a) {
         P w;
         if (a.w) w = load_piece<ET, W>(static_cast<const ET*>(a.w) + c, a.H - c);
 #pragma unroll
-        for (int i = 0; i < W; ++i) y[i] = (float)h[i] * s * (a.w ? (float)w[i] : 1.f);
+        for (int i = 0; i < W; ++i) y[i] = scaled<sizeof(ET) == 2>((float)h[i], a.w ? (float)w[i] : 1.f, s);
       }
       put_piece<ET, F, W>(a, m, c, y);
     }
@@ -233,7 +266,7 @@ __global__ void __launch_bounds__(threads_of(TPR)) qmoe_rms_norm_grad(const Norm
         v[0] = fmaf((float)h[j][i], (float)h[j][i], v[0]);
         v[1] = fmaf((float)g[j][i] * (float)w[j][i], (float)h[j][i], v[1]);
       }
-    row_sum<2, TPR>(v, red, turn);
+    row_sum<float, 2, TPR>(v, red, turn);
     const float s = 1.f / sqrtf(v[0] / (float)a.H + a.eps), mean = v[1] * s / (float)a.H;
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
@@ -245,7 +278,7 @@ __global__ void __launch_bounds__(threads_of(TPR)) qmoe_rms_norm_grad(const Norm
         o[i] = (ET)fmaf(s, gi * (float)w[j][i] - n * mean, (float)d[j][i]);
         acc[j][i] = fmaf(gi, n, acc[j][i]);
       }
-      if (a.dh) store_piece<ET, W>(static_cast<ET*>(a.dh) + m * a.H + c, H - c, o);
+      if (a.dh) store_piece<ET, W>(static_cast<ET*>(a.dh) + m * a.H + c, H - c, o, a.stream);
     }
   }
   if (!a.dw) return;
@@ -296,7 +329,7 @@ __global__ void __launch_bounds__(1024) qmoe_rms_norm_grad_long(const NormGrad a
         v[1] = fmaf((float)g[i] * (w ? (float)wp[i] : 1.f), (float)h[i], v[1]);
       }
     }
-    row_sum<2, TPR>(v, red, turn);
+    row_sum<float, 2, TPR>(v, red, turn);
     const float s = 1.f / sqrtf(v[0] / (float)a.H + a.eps), mean = v[1] * s / (float)a.H;
     if (a.dw && threadIdx.x == 0) rstd[m] = s;
     if (!a.dh) continue;
@@ -309,7 +342,7 @@ __global__ void __launch_bounds__(1024) qmoe_rms_norm_grad_long(const NormGrad a
 #pragma unroll
       for (int i = 0; i < W; ++i)
         o[i] = (ET)fmaf(s, (float)g[i] * (w ? (float)wp[i] : 1.f) - (float)h[i] * s * mean, (float)d[i]);
-      store_piece<ET, W>(static_cast<ET*>(a.dh) + m * a.H + c, n, o);
+      store_piece<ET, W>(static_cast<ET*>(a.dh) + m * a.H + c, n, o, a.stream);
     }
   }
 }
@@ -422,8 +455,9 @@ void with_shape(const NormShape& s, G f) {
 }
 
 template <typename ET, int F>
-hipError_t norm_t(const Norm& a, hipStream_t st) {
+hipError_t norm_t(Norm a, hipStream_t st) {
   constexpr int W = 16 / (int)sizeof(ET);
+  a.stream = a.M * a.H * (long)((a.y ? sizeof(ET) : 0) + (a.sum ? sizeof(ET) : 0) + (F >= 0 ? 1 : 0)) >= kStreamBytes;
   const NormShape s = norm_shape(a.M, (a.H + W - 1) / W, 4096);
   const dim3 grid(norm_grid(a.M, s)), block(threads_of(s.threads));
   if (s.np == 0) {
@@ -446,8 +480,9 @@ hipError_t norm_format(const Norm& a, hipStream_t st) {
 long padded(long H) { return (H + 3) / 4 * 4; }
 
 template <typename ET>
-hipError_t norm_grad_t(const NormGrad& a, hipStream_t st) {
+hipError_t norm_grad_t(NormGrad a, hipStream_t st) {
   constexpr int W = 16 / (int)sizeof(ET);
+  a.stream = a.dh && a.M * a.H * (long)sizeof(ET) >= kStreamBytes;
   const NormShape s = norm_shape(a.M, (a.H + W - 1) / W, kMostGrad<ET>);
   const long ldp = padded(a.H);
   const float* partial = a.partial;

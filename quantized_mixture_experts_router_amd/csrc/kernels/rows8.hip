@@ -10,13 +10,13 @@ namespace {
 // A thread per piece of W columns (16 bytes), `per` threads a row (a power of two
 // up to 256, the rest of the row in blockIdx.y): the lanes of one block of columns,
 // neighbours in a wavefront, find its largest magnitude.
-// 4096 x 14336 bfloat16: 35.5 us for 178 MB, 5.0 TB/s; 16 x 4096: 2.2 us.  One row
-// a thread: two, four and eight rows in flight take 37, 38 and 39 us there and
-// 2.5, 3.2 and 4.6 us here.
+// 4096 x 14336 bfloat16: 32 us for 178 MB, 5.5 TB/s; 16 x 4096: 2.2 us.  One row
+// a thread: two, four and eight rows in flight take 5, 7 and 9 % longer there
+// and 2.5, 3.2 and 4.6 us here.
 template <typename ET, int F>
 __global__ void __launch_bounds__(256) qmoe_quantize_rows(const ET* __restrict__ x, long M, int N, int block_log,
-                                                          int per_log, int b0, uint8_t* __restrict__ codes,
-                                                          float* __restrict__ scales) {
+                                                          int per_log, int b0, int stream,
+                                                          uint8_t* __restrict__ codes, float* __restrict__ scales) {
   constexpr int W = 16 / (int)sizeof(ET), WL = W == 8 ? 3 : 2;
   const int c = (((int)blockIdx.y << per_log) + ((int)threadIdx.x & ((1 << per_log) - 1))) * W;
   const long m = ((long)(b0 + blockIdx.x) << (8 - per_log)) + (threadIdx.x >> per_log);
@@ -33,20 +33,20 @@ __global__ void __launch_bounds__(256) qmoe_quantize_rows(const ET* __restrict__
   }
   const uint32_t s = r8_scale_bits<F>(lanes_max(top, block_log - WL));
   if (!here) return;
-  store_codes<F, W>(codes + m * N + c, n, v, r8_inverse(s));
+  store_codes<F, W>(codes + m * N + c, n, v, r8_inverse(s), stream);
   const int blocks = (N + (1 << block_log) - 1) >> block_log;
   if ((c & ((1 << block_log) - 1)) == 0) scales[m * blocks + (c >> block_log)] = __uint_as_float(s);
 }
 
 // A thread per piece of W columns of an output row, as above.  4096 x 14336 to
-// bfloat16: 42 us for 178 MB; 2047 rows of 2048 to 12282 float16 rows 16.8 us, where
-// 50 MB are written, at 3.0 TB/s, and 4 read.
+// bfloat16: 27 us for 178 MB, 6.5 TB/s; 2047 rows of 2048 to 12282 float16 rows 15 us,
+// where 50 MB are written, at 3.3 TB/s, and 4 read.
 template <typename ET, int F>
 __global__ void __launch_bounds__(256) qmoe_dequantize_rows(const uint8_t* __restrict__ codes,
                                                             const float* __restrict__ scales,
                                                             const int* __restrict__ perm, int k, long M, int N,
-                                                            int block_log, int per_log, int b0, ET* __restrict__ out,
-                                                            long ld) {
+                                                            int block_log, int per_log, int b0, int stream,
+                                                            ET* __restrict__ out, long ld) {
   constexpr int W = 16 / (int)sizeof(ET);
   const int c = (((int)blockIdx.y << per_log) + ((int)threadIdx.x & ((1 << per_log) - 1))) * W;
   const long m = ((long)(b0 + blockIdx.x) << (8 - per_log)) + (threadIdx.x >> per_log);
@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(256) qmoe_dequantize_rows(const uint8_t* __res
   typename RowPiece<ET, W>::type o;
 #pragma unroll
   for (int i = 0; i < W; ++i) o[i] = (ET)v[i];
-  store_piece<ET, W>(out + m * ld + c, (int)min(ld - c, (long)W), o);
+  store_piece<ET, W>(out + m * ld + c, (int)min(ld - c, (long)W), o, stream);
 }
 
 // Threads a row (log2, at least `least`), launches' workgroups and the rest of
@@ -89,7 +89,7 @@ hipError_t quantize_t(const void* x, long M, long N, const Rows8& q, hipStream_t
   const PieceGrid g = piece_grid(M, (N + W - 1) / W, q.block_log - WL);
   return in_launches(g.x, [&](int b0, unsigned n) {
     with_format(q.format, [&](auto f) {
-      hipLaunchKernelGGL((qmoe_quantize_rows<ET, decltype(f)::value>), dim3(n, g.y), dim3(256), 0, st, (const ET*)x, M, (int)N, q.block_log, g.per_log, b0, q.codes, q.scales);
+      hipLaunchKernelGGL((qmoe_quantize_rows<ET, decltype(f)::value>), dim3(n, g.y), dim3(256), 0, st, (const ET*)x, M, (int)N, q.block_log, g.per_log, b0, M * N >= kStreamBytes, q.codes, q.scales);
     });
   });
 }
@@ -100,7 +100,7 @@ hipError_t dequantize_t(const Rows8& q, const int* perm, int k, long M, long N, 
   const PieceGrid g = piece_grid(M, (ld + W - 1) / W, 0);
   return in_launches(g.x, [&](int b0, unsigned n) {
     with_format(q.format, [&](auto f) {
-      hipLaunchKernelGGL((qmoe_dequantize_rows<ET, decltype(f)::value>), dim3(n, g.y), dim3(256), 0, st, q.codes, q.scales, perm, k, M, (int)N, q.block_log, g.per_log, b0, (ET*)out, ld);
+      hipLaunchKernelGGL((qmoe_dequantize_rows<ET, decltype(f)::value>), dim3(n, g.y), dim3(256), 0, st, q.codes, q.scales, perm, k, M, (int)N, q.block_log, g.per_log, b0, M * ld * (long)sizeof(ET) >= kStreamBytes, (ET*)out, ld);
     });
   });
 }

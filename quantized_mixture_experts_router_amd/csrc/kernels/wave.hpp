@@ -45,11 +45,13 @@ __device__ __forceinline__ double dpp_add(double v) {
   const uint64_t o = (uint64_t)dpp_from<CTRL>((uint32_t)(u >> 32)) << 32 | dpp_from<CTRL>((uint32_t)u);
   return v + __builtin_bit_cast(double, o);
 }
+// Sum over 8, 16, 32 or 64 lanes that differ in the low bits of their number.
+template <int LANES = 64>
 __device__ __forceinline__ double wave_sum_double(double v) {
   v = dpp_add<kDppXor1>(v);
   v = dpp_add<kDppXor2>(v);
   v = dpp_add<kDppHalf>(v);
-  v = dpp_add<kDppRow>(v);
+  if constexpr (LANES > 8) v = dpp_add<kDppRow>(v);
   auto halves = [](double x, auto swap) {
     const uint64_t u = __builtin_bit_cast(uint64_t, x);
     uint32_t al = (uint32_t)u, ah = (uint32_t)(u >> 32), bl = al, bh = ah;
@@ -57,8 +59,9 @@ __device__ __forceinline__ double wave_sum_double(double v) {
     swap(ah, bh);
     return __builtin_bit_cast(double, (uint64_t)ah << 32 | al) + __builtin_bit_cast(double, (uint64_t)bh << 32 | bl);
   };
-  v = halves(v, [](uint32_t& a, uint32_t& b) { swap16(a, b); });
-  return halves(v, [](uint32_t& a, uint32_t& b) { swap32(a, b); });
+  if constexpr (LANES > 16) v = halves(v, [](uint32_t& a, uint32_t& b) { swap16(a, b); });
+  if constexpr (LANES > 32) v = halves(v, [](uint32_t& a, uint32_t& b) { swap32(a, b); });
+  return v;
 }
 
 }  // namespace qmoe

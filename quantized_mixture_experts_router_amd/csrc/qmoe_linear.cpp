@@ -11,6 +11,7 @@
 #include <algorithm>
 #include <cstdio>
 
+#include "kernels/launches.h"
 #include "kernels/linear.h"
 #include "qmoe_checks.h"
 
@@ -230,8 +231,19 @@ qmoe_status check_grads(const qmoe_tensor* grad_output, const qmoe_tensor* input
 }
 
 // One product: matrix kernel, and the finishing pass when it ran in ranges.
+// An output of kStreamBytes and more is stored past the caches.  Same card, in turn,
+// us with / without: 8-bit pre-activations beside the output of 12288 rows in 64 groups
+// 220 / 235, of 16384 rows in 16 groups 231 / 272; weight gradients of 64 groups of 2816 x
+// 2048 (738 MB) 313 / 321, of 8 of 4096 x 4096 with dx 85 / 91; dx of 12288 x 2048 234 /
+// 254; a forward and the next layer's of 12288 rows in 64 groups 330 / 350.  Smaller ones
+// are read again from the caches (two layers of 1024 x 2048: 30.5 / 28.9).
 bool run_product(int type, int mode, const LinearPlan& pl, LinearGemm g, float* partial, hipStream_t s) {
   g.splits = pl.splits;
+  const int64_t es = type == LIN_F32 ? 4 : 2, z = (int64_t)g.M * g.N;
+  const int64_t y = g.act.type == QMOE_ACT_SWIGLU ? z / 2 : z;
+  const int64_t out = mode == LIN_DW ? es * g.G * g.N * g.K : mode == LIN_DX ? es * g.M * g.K
+                      : es * y + (g.pre ? es * z : 0) + (g.pre8.codes ? z : 0);
+  g.stream = out >= kStreamBytes;
   g.partial = partial;
   if (launch_linear(type, mode, pl.tile, g, s) != hipSuccess) return false;
   return pl.splits == 1 || launch_linear_finish(type, mode, g, s) == hipSuccess;

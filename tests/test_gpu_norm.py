@@ -140,6 +140,16 @@ def test_zero_rows_and_what_is_not_finite(torch, dt):
     assert torch.allclose(gx[0].double(), torch.full((72,), 1000.0, device="cuda", dtype=torch.float64), rtol=2.0 ** -7)
 
 
+def test_squares_beyond_float32(torch):
+    for dt in (torch.float32, torch.bfloat16):
+        for H in (72, 5000, 40000):
+            x = torch.ones(3, H, dtype=dt, device="cuda")
+            x[1] = 1e25
+            y, _, c, s = qm.rms_norm(x, torch.ones(H, dtype=dt, device="cuda"), None, 1e-6, "e4m3", 64)
+            assert not y[1].any() and (s[1] == 1).all() and not c[1].view(torch.uint8).any()
+            assert torch.equal(y[0], y[2]) and (y[0].float() - 1).abs().max() < 1e-6
+
+
 def test_empty(torch):
     w = torch.ones(8, device="cuda")
     x = torch.zeros(0, 8, device="cuda")
