@@ -20,10 +20,12 @@ hipError_t in_launches(long blocks, F f) {
   return hipSuccess;
 }
 
-// A pass that writes this much (what the eight L2 caches hold) stores it past
-// them: 4096 x 14336 from 8 bits to bfloat16 27 us (39 through them), to 8 bits 32
-// (35), a norm of 8192 x 4096 with residual 48 (50), with 8 bits 56 (58).  What is smaller is
-// read again from the caches (4096 x 4096 to 8 bits and back 19.6 us, 21.3 past them).
+// A pass that writes this much (what the eight L2 caches hold) stores its rows past
+// the caches: 4096 x 14336 from 8 bits to bfloat16 27 us (39 through them), a norm of
+// 8192 x 4096 with residual 48 (50).  Smaller rows are read again from the caches (4096 x
+// 4096 to 8 bits and back 18.8 us, 21.3 past them), and so are 8-bit codes of any size
+// by what follows: 4096 x 14336 to 8 bits and back 57 us, 68 with the codes past
+// them, a norm of 8192 x 4096 with 8 bits and their values 70 and 78.
 constexpr long kStreamBytes = 32l << 20;
 
 }  // namespace qmoe

@@ -115,7 +115,7 @@ __device__ __forceinline__ void put_piece(const Norm& a, long m, int c, const fl
     for (int i = 0; i < W; ++i) top = max(top, abs_bits(y[i]));
     const uint32_t s = r8_scale_bits<F>(lanes_max(top, min(bl - (W == 8 ? 3 : 2), lanes)));
     if (n > 0) {
-      store_codes<F, W>(a.q.codes + m * a.H + c, n, y, r8_inverse(s), a.stream);
+      store_codes<F, W>(a.q.codes + m * a.H + c, n, y, r8_inverse(s));
       if ((c & ((1 << bl) - 1)) == 0) a.q.scales[m * ((a.H + (1 << bl) - 1) >> bl) + (c >> bl)] = __uint_as_float(s);
     }
   }

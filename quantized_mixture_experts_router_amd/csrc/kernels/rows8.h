@@ -20,7 +20,8 @@ hipError_t launch_quantize_rows(int type, const void* x, long M, long N, const R
 
 // out[m] = the values of row m, or (perm) of row perm[m] / k (entries outside
 // [0, M): zeros), rows of ld >= N elements, zeros from N on.  M: rows of out.
+// soon: the caller reads them right away, they stay in the caches whatever their size.
 hipError_t launch_dequantize_rows(int type, const Rows8& q, const int* perm, int k, long M, long N, void* out, long ld,
-                                  hipStream_t st);
+                                  bool soon, hipStream_t st);
 
 }  // namespace qmoe

@@ -10,13 +10,13 @@ namespace {
 // A thread per piece of W columns (16 bytes), `per` threads a row (a power of two
 // up to 256, the rest of the row in blockIdx.y): the lanes of one block of columns,
 // neighbours in a wavefront, find its largest magnitude.
-// 4096 x 14336 bfloat16: 32 us for 178 MB, 5.5 TB/s; 16 x 4096: 2.2 us.  One row
+// 4096 x 14336 bfloat16: 35.5 us for 178 MB, 5.0 TB/s; 16 x 4096: 2.2 us.  One row
 // a thread: two, four and eight rows in flight take 5, 7 and 9 % longer there
 // and 2.5, 3.2 and 4.6 us here.
 template <typename ET, int F>
 __global__ void __launch_bounds__(256) qmoe_quantize_rows(const ET* __restrict__ x, long M, int N, int block_log,
-                                                          int per_log, int b0, int stream,
-                                                          uint8_t* __restrict__ codes, float* __restrict__ scales) {
+                                                          int per_log, int b0, uint8_t* __restrict__ codes,
+                                                          float* __restrict__ scales) {
   constexpr int W = 16 / (int)sizeof(ET), WL = W == 8 ? 3 : 2;
   const int c = (((int)blockIdx.y << per_log) + ((int)threadIdx.x & ((1 << per_log) - 1))) * W;
   const long m = ((long)(b0 + blockIdx.x) << (8 - per_log)) + (threadIdx.x >> per_log);
@@ -33,7 +33,7 @@ __global__ void __launch_bounds__(256) qmoe_quantize_rows(const ET* __restrict__
   }
   const uint32_t s = r8_scale_bits<F>(lanes_max(top, block_log - WL));
   if (!here) return;
-  store_codes<F, W>(codes + m * N + c, n, v, r8_inverse(s), stream);
+  store_codes<F, W>(codes + m * N + c, n, v, r8_inverse(s));
   const int blocks = (N + (1 << block_log) - 1) >> block_log;
   if ((c & ((1 << block_log) - 1)) == 0) scales[m * blocks + (c >> block_log)] = __uint_as_float(s);
 }
@@ -89,18 +89,19 @@ hipError_t quantize_t(const void* x, long M, long N, const Rows8& q, hipStream_t
   const PieceGrid g = piece_grid(M, (N + W - 1) / W, q.block_log - WL);
   return in_launches(g.x, [&](int b0, unsigned n) {
     with_format(q.format, [&](auto f) {
-      hipLaunchKernelGGL((qmoe_quantize_rows<ET, decltype(f)::value>), dim3(n, g.y), dim3(256), 0, st, (const ET*)x, M, (int)N, q.block_log, g.per_log, b0, M * N >= kStreamBytes, q.codes, q.scales);
+      hipLaunchKernelGGL((qmoe_quantize_rows<ET, decltype(f)::value>), dim3(n, g.y), dim3(256), 0, st, (const ET*)x, M, (int)N, q.block_log, g.per_log, b0, q.codes, q.scales);
     });
   });
 }
 
 template <typename ET>
-hipError_t dequantize_t(const Rows8& q, const int* perm, int k, long M, long N, void* out, long ld, hipStream_t st) {
+hipError_t dequantize_t(const Rows8& q, const int* perm, int k, long M, long N, void* out, long ld, bool soon,
+                        hipStream_t st) {
   constexpr int W = 16 / (int)sizeof(ET);
   const PieceGrid g = piece_grid(M, (ld + W - 1) / W, 0);
   return in_launches(g.x, [&](int b0, unsigned n) {
     with_format(q.format, [&](auto f) {
-      hipLaunchKernelGGL((qmoe_dequantize_rows<ET, decltype(f)::value>), dim3(n, g.y), dim3(256), 0, st, q.codes, q.scales, perm, k, M, (int)N, q.block_log, g.per_log, b0, M * ld * (long)sizeof(ET) >= kStreamBytes, (ET*)out, ld);
+      hipLaunchKernelGGL((qmoe_dequantize_rows<ET, decltype(f)::value>), dim3(n, g.y), dim3(256), 0, st, q.codes, q.scales, perm, k, M, (int)N, q.block_log, g.per_log, b0, !soon && M * ld * (long)sizeof(ET) >= kStreamBytes, (ET*)out, ld);
     });
   });
 }
@@ -114,10 +115,10 @@ hipError_t launch_quantize_rows(int type, const void* x, long M, long N, const R
 }
 
 hipError_t launch_dequantize_rows(int type, const Rows8& q, const int* perm, int k, long M, long N, void* out, long ld,
-                                  hipStream_t st) {
-  if (type == ROW_F32) return dequantize_t<float>(q, perm, k, M, N, out, ld, st);
-  if (type == ROW_F16) return dequantize_t<_Float16>(q, perm, k, M, N, out, ld, st);
-  return dequantize_t<__bf16>(q, perm, k, M, N, out, ld, st);
+                                  bool soon, hipStream_t st) {
+  if (type == ROW_F32) return dequantize_t<float>(q, perm, k, M, N, out, ld, soon, st);
+  if (type == ROW_F16) return dequantize_t<_Float16>(q, perm, k, M, N, out, ld, soon, st);
+  return dequantize_t<__bf16>(q, perm, k, M, N, out, ld, soon, st);
 }
 
 }  // namespace qmoe

@@ -141,14 +141,14 @@ __device__ __forceinline__ uint32_t r8_encode4(const f32x4& v, float inv) {
 
 // Codes of W (2, 4 or 8) values behind p, n of them in the row.
 template <int F, int W>
-__device__ __forceinline__ void store_codes(uint8_t* p, int n, const float (&v)[W], float inv, int stream = 0) {
+__device__ __forceinline__ void store_codes(uint8_t* p, int n, const float (&v)[W], float inv) {
   uint32_t u[(W + 3) / 4];
   if constexpr (W == 2) u[0] = r8_encode4<F>(v[0], v[1], 0.f, 0.f, inv);
 #pragma unroll
   for (int i = 0; i < W / 4; ++i) u[i] = r8_encode4<F>(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3], inv);
   typename RowPiece<uint8_t, W>::type t;
   __builtin_memcpy(&t, u, W);
-  store_piece<uint8_t, W>(p, n, t, stream);
+  store_piece<uint8_t, W>(p, n, t);
 }
 // Values of the W codes behind p, n of them in the row (zeros past its end),
 // within the range of ET.

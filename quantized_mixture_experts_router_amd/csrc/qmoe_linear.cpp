@@ -395,7 +395,7 @@ qmoe_status backward(const LinPlan& p, const qmoe_tensor* grad_output, const qmo
   if (p.x8 && gw && p.M > 0) {
     if (launch_dequantize_rows(row_type(weights->dtype), rows8_of(input, h.input_scales, h.block_size),
                                h.perm ? static_cast<const int*>(h.perm->data) : nullptr,
-                               (int)(p.M / input->dims[0]), p.M, p.K, ws + p.off_x, p.Kp, s) != hipSuccess)
+                               (int)(p.M / input->dims[0]), p.M, p.K, ws + p.off_x, p.Kp, true, s) != hipSuccess)
       return QMOE_ERR_HIP;
     g.x = ws + p.off_x;
   }

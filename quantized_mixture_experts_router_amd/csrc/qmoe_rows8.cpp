@@ -42,7 +42,7 @@ qmoe_status qmoe_dequantize_rows(const qmoe_tensor* codes, const qmoe_tensor* sc
   if (st != QMOE_OK) return st;
   return launch_dequantize_rows(row_type(output->dtype), rows8_of(codes, scales, block_size),
                                 perm ? static_cast<const int*>(perm->data) : nullptr, (int)(M / T), M, N,
-                                data_of(output), N, reinterpret_cast<hipStream_t>(stream)) == hipSuccess
+                                data_of(output), N, false, reinterpret_cast<hipStream_t>(stream)) == hipSuccess
              ? QMOE_OK
              : QMOE_ERR_HIP;
 }
