@@ -76,7 +76,7 @@ __device__ __forceinline__ double reciprocal(double d) {
 // of them the 64-bit exponentials): reductions stay in registers, ranks of groups
 // are counted by all lanes, and a round of the selection is one reduction, a compare
 // a register (whose ballots give the lowest expert that holds the largest key) and
-// a write to one lane.  16384 x 256 logits, 6 out of 5 of 16 groups, softmax: 17.7
+// a write to one lane.  16384 x 256 logits, 6 out of 5 of 16 groups, softmax: 17.0
 // us (30.5 with reductions and scores through LDS and library exponentials) where
 // its bytes take 3.5; 16 x 128, sigmoid: 3.9 us.
 // k <= 64 (else MANY: pick r in lane r % 64 of register r / 64).
@@ -84,7 +84,7 @@ template <int V, bool MANY>
 __global__ void __launch_bounds__(256) qmoe_route_scored(const float* __restrict__ logits,
                                                          const float* __restrict__ bias, int T, RouteScored a, int b0,
                                                          int* __restrict__ idx, float* __restrict__ w) {
-  __shared__ float lds[4][64 * V];
+  __shared__ int lds[4][64 * V];  // per wavefront: ranks, then groups' ranks, then the scores' bits
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = lane_id();
   const int t = (b0 + blockIdx.x) * 4 + wave;
   if (t >= T) return;
@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(256) qmoe_route_scored(const float* __restrict
     c[j] = v[j] == -INFINITY ? kNone : key_of(x);
   }
   if (a.kept < a.groups) {
-    int* s = reinterpret_cast<int*>(lds[wave]);
+    int* s = lds[wave];
 #pragma unroll
     for (int j = 0; j < V; ++j) s[lane + 64 * j] = c[j];
     // (one wavefront's own LDS words: written and read in program order)
@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(256) qmoe_route_scored(const float* __restrict
     __builtin_amdgcn_wave_barrier();
   }
 #pragma unroll
-  for (int j = 0; j < V; ++j) lds[wave][lane + 64 * j] = p[j];
+  for (int j = 0; j < V; ++j) lds[wave][lane + 64 * j] = __float_as_int(p[j]);
   constexpr int KV = MANY ? V : 1;
   int pe[KV];
 #pragma unroll
@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(256) qmoe_route_scored(const float* __restrict
   float x[KV], sum = 0.f;
 #pragma unroll
   for (int j = 0; j < KV; ++j) {
-    x[j] = pe[j] < 0 ? 0.f : lds[wave][pe[j]];
+    x[j] = pe[j] < 0 ? 0.f : __int_as_float(lds[wave][pe[j]]);
     sum += x[j];
   }
   if (a.normalize) {

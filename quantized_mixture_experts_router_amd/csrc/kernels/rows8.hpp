@@ -98,7 +98,7 @@ template <typename ET, int F>
 __device__ __forceinline__ bool r8_may_pass(float scale) {
   constexpr float from = std::is_same<ET, _Float16>::value ? (F == R8_INT8 ? 1024.f : 256.f)
                                                            : (F == R8_INT8 ? 0x1p122f : 0x1p120f);
-  return scale >= from;
+  return fabsf(scale) >= from;
 }
 
 // W consecutive elements of a row of which n are left, at element alignment
