@@ -699,7 +699,9 @@ qmoe_status qmoe_route_scored(const qmoe_tensor* router_probs, const qmoe_tensor
 /* Gradient of qmoe_route_scored at the logits: grad_router_probs [T, E] from
  * grad_weights [T, k], with the forward's router_probs and indices (int32 or
  * int64; attrs->k is not read).  The selection is constant, so the bias has no
- * gradient.  Masked experts get 0, as do slots with an index outside [0, E). */
+ * gradient.  Masked experts get 0, as do slots with an index outside [0, E).
+ * Scores (0 where float32 has 0 for them, else not rounded), their sums and the
+ * differences that cancel are float64; the result is rounded once. */
 qmoe_status qmoe_route_scored_backward(const qmoe_tensor* grad_weights, const qmoe_tensor* router_probs,
                                        const qmoe_tensor* indices, const qmoe_route_attrs* attrs,
                                        const qmoe_tensor* grad_router_probs, void* stream);

@@ -221,11 +221,15 @@ __global__ void __launch_bounds__(256) qmoe_route_scored(const float* __restrict
 }
 
 // One wavefront per token.  With s the scores, u = s at the slots (0 for masked
-// or outside ones), S = sum u, g the slots' gradients times scale and D_e the sum
-// over the slots of e:
-//   as they are:    sigmoid   gl_e = D_e s_e (1 - s_e)      softmax   gl_e = s_e (D_e - sum_i u_i g_i)
+// or outside ones), S = sum u, g the slots' gradients and D_e the sum over the
+// slots of e:
+//   as they are:    sigmoid   gl_e = scale D_e s_e (1 - s_e)      softmax   gl_e = scale s_e (D_e - sum_i u_i g_i)
 //   renormalised:   with g_i - sum_i u_i g_i / S in the place of g_i and s_e / S in the place of the first s_e, where the
 //                   softmax's sum is 0 by itself (all 0 where S is)
+// The differences cancel: renormalised, one slot has a gradient of 0, and where one
+// holds nearly all of S (or of the softmax) what is left is far below the g's.  So
+// scores, sums and differences are float64, and a result is rounded once, at its
+// end.  (A score that is 0 in float32, as the forward pass has it, is 0.)
 // A lane adds up its experts' slots in slot order (no atomics; the same expert
 // twice counts twice).
 template <int V>
@@ -233,81 +237,88 @@ __global__ void __launch_bounds__(256) qmoe_route_scored_grad(const float* __res
                                                               const float* __restrict__ logits,
                                                               const void* __restrict__ idx, bool idx64, int T,
                                                               RouteScored a, int b0, float* __restrict__ gl) {
-  extern __shared__ char smem[];  // per wavefront: k experts, k values
+  extern __shared__ double smem[];  // per wavefront: k values; behind all of those, per wavefront: k experts
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = lane_id();
-  int* se = reinterpret_cast<int*>(smem) + wave * 2 * a.k;
-  float* sv = reinterpret_cast<float*>(se + a.k);
+  double* sv = smem + wave * a.k;
+  int* se = reinterpret_cast<int*>(smem + 4 * a.k) + wave * a.k;
   const int t = (b0 + blockIdx.x) * 4 + wave;
   if (t >= T) return;
   const float* row = logits + (long)t * a.E;
   float v[V];
   load_logits<V>(row, a.E, lane, v);
-  float top = 0.f, inv = 1.f;
-  if (!a.sigmoid) {
+  double e[V], inv = 1.0;
+  float top = 0.f;
+  if (a.sigmoid) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) e[j] = (double)fmaxf(-fabsf(v[j]), -110.f);
+    exp_below<V>(e);
+  } else {
     int m = key_of(v[0]);
-    float sum = 0.f;
 #pragma unroll
     for (int j = 1; j < V; ++j) m = max(m, key_of(v[j]));
-    m = wave_max_int(m);
-    top = m == kNone ? 0.f : of_key(m);
+    top = fmaxf(of_key(wave_max_int(m)), -3.4028234664e38f);
 #pragma unroll
-    for (int j = 0; j < V; ++j) sum += expf(v[j] - top);
-    sum = wave_sum_float(sum);
-    inv = sum > 0.f ? 1.f / sum : 0.f;
+    for (int j = 0; j < V; ++j) e[j] = fmax((double)v[j] - (double)top, -110.0);
+    exp_below<V>(e);
+    double sum = 0.0;
+#pragma unroll
+    for (int j = 0; j < V; ++j) sum += e[j];
+    inv = reciprocal(fmax(wave_sum_double(sum), 1.0));
   }
-  // (sigmoid: e^-|l| keeps the digits of scores near 0 and of 1 - s near 1)
-  auto score = [&](float l) {
-    if (!a.sigmoid) return expf(l - top) * inv;
-    const float e = expf(-fabsf(l));
-    return (l < 0.f ? e : 1.f) / (1.f + e);
+  // The score of logit l, where x = e^-|l| (sigmoid: that keeps the digits of scores near 0 and of 1 - s near 1) or e^(l - top).
+  auto score = [&](float l, double x) {
+    const double s = a.sigmoid ? (l < 0.f ? x : 1.0) * reciprocal(1.0 + x) : x * inv;
+    return (float)s > 0.f ? s : 0.0;
   };
-  float S = 0.f, dot = 0.f;
+  double S = 0.0, dot = 0.0;
   for (int s = lane; s < a.k; s += 64) {
     const long at = (long)t * a.k + s;
-    int64_t e = idx64 ? static_cast<const int64_t*>(idx)[at] : static_cast<const int*>(idx)[at];
-    float x = -INFINITY;
-    if (e >= 0 && e < a.E) {
-      x = row[e];
-      x = x != x ? -INFINITY : fminf(x, 3.4028234664e38f);
+    int64_t i = idx64 ? static_cast<const int64_t*>(idx)[at] : static_cast<const int*>(idx)[at];
+    float l = -INFINITY;
+    if (i >= 0 && i < a.E) {
+      l = row[i];
+      l = l != l ? -INFINITY : fminf(l, 3.4028234664e38f);
     }
-    if (x == -INFINITY) e = -1;
-    const float u = e < 0 ? 0.f : score(x), g = e < 0 ? 0.f : gw[at] * a.scale;
-    se[s] = (int)e;
+    if (l == -INFINITY) i = -1;
+    double x[1] = {a.sigmoid ? (double)fmaxf(-fabsf(l), -110.f) : fmax((double)l - (double)top, -110.0)};
+    exp_below<1>(x);
+    const double u = i < 0 ? 0.0 : score(l, x[0]), g = i < 0 ? 0.0 : (double)gw[at];
+    se[s] = (int)i;
     sv[s] = g;
     S += u;
-    dot = fmaf(u, g, dot);
+    dot = fma(u, g, dot);
   }
-  S = wave_sum_float(S);
-  dot = wave_sum_float(dot);
-  float shift = 0.f, mean = dot;
+  S = wave_sum_double(S);
+  dot = wave_sum_double(dot);
+  double shift = 0.0, mean = dot, over = 1.0;
   if (a.normalize) {
-    shift = S > 0.f ? dot / S : 0.f;
-    mean = 0.f;
+    // (a division: u g / u is g where one slot is left)
+    shift = S > 0.0 ? dot / S : 0.0;
+    over = S > 0.0 ? reciprocal(S) : 0.0;
+    mean = 0.0;
   }
   // (one wavefront's own LDS words: written and read in program order)
   __builtin_amdgcn_wave_barrier();
-  float d[V];
+  double d[V];
 #pragma unroll
-  for (int j = 0; j < V; ++j) d[j] = 0.f;
+  for (int j = 0; j < V; ++j) d[j] = 0.0;
   for (int s = 0; s < a.k; ++s) {
-    const int e = se[s];
-    const float x = sv[s] - shift;
+    const int i = se[s];
+    const double x = sv[s] - shift;
 #pragma unroll
     for (int j = 0; j < V; ++j)
-      if (e == lane + 64 * j) d[j] += x;
+      if (i == lane + 64 * j) d[j] += x;
   }
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     if (lane + 64 * j >= a.E) continue;
-    float o = 0.f;
+    double o = 0.0;
     if (v[j] != -INFINITY) {
-      float f = score(v[j]);
-      // (an expert that no slot names may be far above the selection's sum: s / S would pass float32)
-      if (a.normalize) f = S > 0.f && d[j] != 0.f ? f / S : 0.f;
-      if (a.sigmoid) f *= score(-v[j]);
-      o = f * (d[j] - (a.sigmoid ? 0.f : mean));
+      double f = score(v[j], e[j]) * over;
+      if (a.sigmoid) f *= score(-v[j], e[j]);
+      o = f * (d[j] - (a.sigmoid ? 0.0 : mean)) * (double)a.scale;
     }
-    gl[(long)t * a.E + lane + 64 * j] = o;
+    gl[(long)t * a.E + lane + 64 * j] = (float)o;
   }
 }
 
@@ -344,7 +355,7 @@ hipError_t launch_route_scored(const float* logits, const float* bias, int T, co
 
 hipError_t launch_route_scored_grad(const float* gw, const float* logits, const void* idx, bool idx64, int T,
                                     const RouteScored& a, float* gl, hipStream_t st) {
-  const size_t lds = (size_t)4 * 2 * a.k * 4;
+  const size_t lds = (size_t)4 * a.k * (sizeof(double) + sizeof(int));
   return in_launches(((long)T + 3) / 4, [&](int b0, unsigned n) {
     const dim3 grid(n), block(256);
 #define QMOE_CALL(VV) \
