@@ -634,8 +634,8 @@ qmoe_status qmoe_dequantize_rows(const qmoe_tensor* codes, const qmoe_tensor* sc
  * rounded to T, and / or to codes and scales in 8 bits (codes and scales both or
  * neither; from the float32 result; block_size is read with them).  epsilon > 0
  * and finite (QMOE_ERR_ATTR).  Squares are float32: rows whose squares pass its
- * range give zeros (NaN where sum weight passes it too); a NaN makes its row NaN,
- * an infinity its own element, beside zeros.  M <= 2^30, H <= 2^20 (QMOE_ERR_UNSUPPORTED). */
+ * range give zeros; a NaN makes its row NaN, an infinity its own element, beside
+ * zeros.  M <= 2^30, H <= 2^20 (QMOE_ERR_UNSUPPORTED). */
 qmoe_status qmoe_rms_norm(const qmoe_tensor* input, const qmoe_tensor* residual, const qmoe_tensor* weight,
                           float epsilon, const qmoe_tensor* sum, const qmoe_tensor* output, const qmoe_tensor* codes,
                           const qmoe_tensor* scales, int64_t block_size, void* stream);
@@ -647,8 +647,10 @@ qmoe_status qmoe_rms_norm(const qmoe_tensor* input, const qmoe_tensor* residual,
  *   grad_weight = column sums of grad_output n
  *
  * grad_input [M, H] is the gradient at the forward's input and residual alike;
- * grad_sum [M, H] is what arrives at sum itself (NULL: nothing).  A row whose
- * squares pass float32's range has an unspecified grad_input.  Either result may be NULL; grad_weight needs weight (QMOE_ERR_NULL).  workspace:
+ * grad_sum [M, H] is what arrives at sum itself (NULL: nothing).  Squares and the
+ * terms grad_output weight input of a row's sum are float32: where they leave its
+ * range, the row's grad_input is unspecified.  Either result may be NULL;
+ * grad_weight needs weight (QMOE_ERR_NULL).  workspace:
  * qmoe_rms_norm_backward_workspace_size bytes, 256-byte aligned (NULL when 0). */
 qmoe_status qmoe_rms_norm_backward_workspace_size(const qmoe_tensor* grad_output, const qmoe_tensor* grad_sum,
                                                   const qmoe_tensor* input, const qmoe_tensor* weight, float epsilon,

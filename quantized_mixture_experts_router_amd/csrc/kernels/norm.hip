@@ -80,13 +80,11 @@ __device__ __forceinline__ RowScale row_scale(double ss, int H, float eps) {
   const float hi = (float)y;
   return {hi, (float)(y - (double)hi)};
 }
-// h s w; EXACT: h w is (16-bit types), else its error goes along.
-template <bool EXACT>
+// h s w.  h s first: it is at most sqrt(H), while h w may pass float32's range where the result does not.
 __device__ __forceinline__ float scaled(float h, float w, const RowScale& s) {
-  const float p = h * w;
-  float low = p * s.lo;
-  if constexpr (!EXACT) low = fmaf(fmaf(h, w, -p), s.hi, low);
-  return fmaf(p, s.hi, low);
+  const float n = h * s.hi;
+  const float low = fmaf(h, s.lo, fmaf(h, s.hi, -n));
+  return fmaf(n, w, low * w);
 }
 
 // h of a piece: x + r in float32, rounded to the type (it is what the residual
@@ -176,7 +174,7 @@ __global__ void __launch_bounds__(threads_of(TPR)) qmoe_rms_norm(const Norm a) {
     for (int j = 0; j < NP; ++j) {
       float y[W];
 #pragma unroll
-      for (int i = 0; i < W; ++i) y[i] = scaled<sizeof(ET) == 2>((float)h[j][i], (float)w[j][i], s);
+      for (int i = 0; i < W; ++i) y[i] = scaled((float)h[j][i], (float)w[j][i], s);
       put_piece<ET, F, W>(a, m, c0 + j * TPR * W, y, kLanes);
     }
   }
@@ -216,7 +214,7 @@ __global__ void __launch_bounds__(1024) qmoe_rms_norm_long(const Norm a) {
         P w;
         if (a.w) w = load_piece<ET, W>(static_cast<const ET*>(a.w) + c, a.H - c);
 #pragma unroll
-        for (int i = 0; i < W; ++i) y[i] = scaled<sizeof(ET) == 2>((float)h[i], a.w ? (float)w[i] : 1.f, s);
+        for (int i = 0; i < W; ++i) y[i] = scaled((float)h[i], a.w ? (float)w[i] : 1.f, s);
       }
       put_piece<ET, F, W>(a, m, c, y);
     }
