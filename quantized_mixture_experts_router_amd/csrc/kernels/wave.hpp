@@ -30,9 +30,6 @@ __device__ __forceinline__ uint32_t wave_reduce(uint32_t v, F f) {
 __device__ __forceinline__ int wave_max_int(int v) {
   return (int)wave_reduce((uint32_t)v, [](uint32_t a, uint32_t b) { return (uint32_t)max((int)a, (int)b); });
 }
-__device__ __forceinline__ int wave_min_int(int v) {
-  return (int)wave_reduce((uint32_t)v, [](uint32_t a, uint32_t b) { return (uint32_t)min((int)a, (int)b); });
-}
 __device__ __forceinline__ float wave_sum_float(float v) {
   return __uint_as_float(wave_reduce(__float_as_uint(v), [](uint32_t a, uint32_t b) {
     return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
