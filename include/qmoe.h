@@ -635,7 +635,9 @@ qmoe_status qmoe_dequantize_rows(const qmoe_tensor* codes, const qmoe_tensor* sc
  * neither; from the float32 result; block_size is read with them).  epsilon > 0
  * and finite (QMOE_ERR_ATTR).  Squares are float32: rows whose squares pass its
  * range give zeros; a NaN makes its row NaN, an infinity its own element, beside
- * zeros.  M <= 2^30, H <= 2^20 (QMOE_ERR_UNSUPPORTED). */
+ * zeros.  The order of a row's sums goes by M and H, so a row's last bits may
+ * differ between calls of few (up to 512) and of more rows.  M <= 2^30, H <= 2^20
+ * (QMOE_ERR_UNSUPPORTED). */
 qmoe_status qmoe_rms_norm(const qmoe_tensor* input, const qmoe_tensor* residual, const qmoe_tensor* weight,
                           float epsilon, const qmoe_tensor* sum, const qmoe_tensor* output, const qmoe_tensor* codes,
                           const qmoe_tensor* scales, int64_t block_size, void* stream);
@@ -727,8 +729,8 @@ qmoe_status qmoe_linear_q8(const qmoe_tensor* input, const qmoe_tensor* weights,
  * held in 8 bits once a token ([M / k, K]), stands for the rows that
  * qmoe_dequantize_rows makes of it; grad_input has all M rows.  Values that the
  * codes stand for are exact in T, so the results are those of
- * qmoe_linear_backward on the values (for float16 in its range).  Everything else
- * as qmoe_linear_backward. */
+ * qmoe_linear_backward on the values (for float16 in its range): d, too, is
+ * rounded to a 16-bit T there.  Everything else as qmoe_linear_backward. */
 qmoe_status qmoe_linear_backward_q8_workspace_size(
     const qmoe_tensor* grad_output, const qmoe_tensor* input, const qmoe_tensor* input_scales, const qmoe_tensor* perm,
     const qmoe_tensor* weights, const qmoe_tensor* preact, const qmoe_tensor* preact_scales, int64_t block_size,

@@ -163,7 +163,8 @@ def route_scored(logits, k, kind="softmax", bias=None, groups=1, kept=1, group_t
 
 
 def route_scored_grad(grad_w, logits, idx, kind="softmax", normalize=0, scale=1.0):
-    """Gradient at the logits, the selection constant, by the chain rule through the scores (as rounded to float32)."""
+    """Gradient at the logits, the selection constant, by the chain rule through the scores (as rounded to float32; the
+    library does not round them here)."""
     T, E = logits.shape
     s, off = scores(logits, kind)
     s = s.astype(np.float32).astype(np.float64)

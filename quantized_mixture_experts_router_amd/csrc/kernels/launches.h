@@ -24,8 +24,11 @@ hipError_t in_launches(long blocks, F f) {
 // the caches: 4096 x 14336 from 8 bits to bfloat16 27 us (39 through them), a norm of
 // 8192 x 4096 with residual 48 (50).  Smaller rows are read again from the caches (4096 x
 // 4096 to 8 bits and back 18.8 us, 21.3 past them), and so are 8-bit codes of any size
-// by what follows: 4096 x 14336 to 8 bits and back 57 us, 68 with the codes past
-// them, a norm of 8192 x 4096 with 8 bits and their values 70 and 78.
+// by what follows: 4096 x 14336 to 8 bits and back 31 and 28 us, 33 and 38 with the
+// codes past them, a norm of 8192 x 4096 with 8 bits and their values 54 and 18, 58
+// and 23.  Read much later, with 1 GiB read between, they lose nothing: 31 and 36 us
+// against 33 and 36, 53 and 21 against 57 and 21.  (The codes that leave in a matrix
+// product's epilogue go the way of its output.)
 constexpr long kStreamBytes = 32l << 20;
 
 }  // namespace qmoe

@@ -122,7 +122,7 @@ __device__ __forceinline__ void put_piece(const Norm& a, long m, int c, const fl
 // TPR threads a row, NP pieces of 16 bytes each; a workgroup of 256 threads or
 // more takes a row, or several, and goes on to further ones with the weight in
 // registers.  Bfloat16 with residual: 8192 x 4096 48 us for 268 MB (5.6 TB/s), with
-// 8 bits beside it 57 us for 303 MB; 65536 x 64 8 us (a wavefront a row: 20 us).
+// 8 bits beside it 53 to 55 us for 303 MB; 65536 x 64 8.5 us (a wavefront a row: 20 us).
 template <typename ET, int F, int NP, int TPR>
 __global__ void __launch_bounds__(threads_of(TPR)) qmoe_rms_norm(const Norm a) {
   constexpr int W = 16 / (int)sizeof(ET), R = rows_of(TPR);
@@ -221,8 +221,9 @@ __global__ void __launch_bounds__(1024) qmoe_rms_norm_long(const Norm a) {
   }
 }
 
-// 8192 x 4096 bfloat16 with a gradient at the sum: 44 us for 268 MB and the partial
-// sums, 6.1 TB/s (inputs in part still in the last level of cache), 65536 x 64 10 us.
+// 8192 x 4096 bfloat16 with a gradient at the sum: 50 to 51 us for 268 MB and the
+// partial sums, 5.4 TB/s (inputs in part still in the last level of cache), 65536 x
+// 64 8.8 us; float32 8192 x 4096 93 us for 537 MB.
 // Threads and rows as above; the weight's gradient of a workgroup's rows stays
 // in registers and leaves as one row of partial sums.
 template <typename ET, int NP, int TPR>
@@ -305,7 +306,7 @@ __global__ void __launch_bounds__(threads_of(TPR)) qmoe_rms_norm_grad(const Norm
 
 // Rows too long for registers: read twice; 1 / root mean square of every row
 // into rstd for the weight's gradient, which reads them again.  1024 x 32768
-// bfloat16: 85 us for 268 MB.
+// bfloat16: 63 us for 268 MB, and 27 for the weight's gradient.
 template <typename ET>
 __global__ void __launch_bounds__(1024) qmoe_rms_norm_grad_long(const NormGrad a, float* __restrict__ rstd) {
   constexpr int W = 16 / (int)sizeof(ET), TPR = 1024;
@@ -396,7 +397,7 @@ constexpr int kLongRows = 256;  // rows of partial sums for rows too long for re
 // Few rows: a piece a thread, up to 1024 (16 x 4096 bfloat16 2.9 and with 8 bits 3.4
 // us, with 256 x 2 3.2 and 3.9, with 64 x 8 5.6 and 7.9); many: 256 threads where
 // the row allows (8192 x 4096 48 and 57 us, 128 x 4 48 and 60, 1024 x 1 49 and 72).
-// (512 x 8 in float32 spills 17 registers in the backward pass: 2048 x 16384 82 us for 537 MB.)
+// (512 x 8 in float32 spills 17 registers in the backward pass: 2048 x 16384 104 us for 537 MB.)
 struct NormShape {
   int threads, np;
 };
@@ -419,10 +420,13 @@ unsigned norm_grid(long M, const NormShape& s) {
   const long rows = rows_of(s.threads);
   return (unsigned)std::min<long>((M + rows - 1) / rows, kCUs * (2048 / threads_of(s.threads)));
 }
-// Fewer in the backward pass, each of which leaves a row of partial sums.  When each
-// took one row at a time: 8192 x 4096 (256 x 2) 44 us on two a compute unit, 47 on four,
-// 64 on one; 8192 x 2048 (256 x 1) 28 us on four, 32 on two; 8192 x 1024 (128 x 1)
-// 20 us on four, 22 on eight, 24 on two (two rows at a time: 16 us).
+// Fewer in the backward pass, each of which leaves a row of partial sums.  us with
+// their sum, on 1 / 2 / 4 / 8 workgroups a compute unit, bfloat16: 8192 x 8192 (256 x 4)
+// 115 / 102 / 106 / 117, 8192 x 4096 (256 x 2) 67 / 57 / 57 / 61, 8192 x 2048 (256 x 1)
+// 50 / 34 / 32 / 35, 8192 x 1024 (128 x 1) 25 / 20 / 18 / 22, 65536 x 64 (8 x 1) 13 / 11 /
+// 11 / 13; float32 8192 x 4096 (256 x 4) 100 / 98 / 101 / 104.  On 1 / 2 / 4: bfloat16
+// 4096 x 16384 (512 x 4) 109 / 115 / 127, 512 x 8192 (1024 x 1) 14 / 17 / 18, float32
+// 2048 x 16384 (512 x 8) 108 / 110 / 120.
 unsigned norm_grad_grid(long M, const NormShape& s) {
   const long rows = rows_of(s.threads);
   const long per = s.threads <= 256 && s.np == 1 ? 4 : s.threads <= 256 ? 2 : 1;

@@ -72,13 +72,15 @@ __device__ __forceinline__ double reciprocal(double d) {
 // comparing its score plus bias with others', and two that differ in float32's
 // last bits would change places with the rounding errors of a float32 exponential.
 //
-// Bound by the vector instructions (524 a wavefront below, 83 % of the time, a fifth
-// of them the 64-bit exponentials): reductions stay in registers, ranks of groups
+// Bound by the vector instructions (524 a wavefront below, a fifth of them the 64-bit
+// exponentials; their issue counts 14.6 us of SIMD time if the clock is 2.4 GHz, which
+// was not measured): reductions stay in registers, ranks of groups
 // are counted by all lanes, and a round of the selection is one reduction, a compare
 // a register (whose ballots give the lowest expert that holds the largest key) and
 // a write to one lane.  16384 x 256 logits, 6 out of 5 of 16 groups, softmax: 17.0
-// us (30.5 with reductions and scores through LDS and library exponentials) where
-// its bytes take 3.5; 16 x 128, sigmoid: 3.9 us.
+// us in a row of calls, 19.0 traced alone (30.5 with reductions and scores through
+// LDS and library exponentials) where its bytes take 3.4; 8 out of 4 of 8 groups,
+// sigmoid: 18.5 us; 16 x 128, sigmoid: 4.1 us.
 // k <= 64 (else MANY: pick r in lane r % 64 of register r / 64).
 template <int V, bool MANY>
 __global__ void __launch_bounds__(256) qmoe_route_scored(const float* __restrict__ logits,

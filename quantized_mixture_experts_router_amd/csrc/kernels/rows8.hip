@@ -10,9 +10,9 @@ namespace {
 // A thread per piece of W columns (16 bytes), `per` threads a row (a power of two
 // up to 256, the rest of the row in blockIdx.y): the lanes of one block of columns,
 // neighbours in a wavefront, find its largest magnitude.
-// 4096 x 14336 bfloat16: 35.5 us for 178 MB, 5.0 TB/s; 16 x 4096: 2.2 us.  One row
-// a thread: two, four and eight rows in flight take 5, 7 and 9 % longer there
-// and 2.5, 3.2 and 4.6 us here.
+// 4096 x 14336 bfloat16: 30 to 33 us for 178 MB, 5.4 to 5.9 TB/s; 16 x 4096: 2.5 us.
+// One row a thread: two, four and eight rows in flight took 5, 7 and 9 % longer there
+// and 2.5, 3.2 and 4.6 us against 2.2 here.
 template <typename ET, int F>
 __global__ void __launch_bounds__(256) qmoe_quantize_rows(const ET* __restrict__ x, long M, int N, int block_log,
                                                           int per_log, int b0, uint8_t* __restrict__ codes,
@@ -39,8 +39,8 @@ __global__ void __launch_bounds__(256) qmoe_quantize_rows(const ET* __restrict__
 }
 
 // A thread per piece of W columns of an output row, as above.  4096 x 14336 to
-// bfloat16: 27 us for 178 MB, 6.5 TB/s; 2047 rows of 2048 to 12282 float16 rows 15 us,
-// where 50 MB are written, at 3.3 TB/s, and 4 read.
+// bfloat16: 27 us for 178 MB, 36 (5.0 TB/s) with nothing of them in the caches; 2047
+// rows of 2048 to 12282 float16 rows 13.7 us, where 50 MB are written, at 3.7 TB/s, and 4 read.
 template <typename ET, int F>
 __global__ void __launch_bounds__(256) qmoe_dequantize_rows(const uint8_t* __restrict__ codes,
                                                             const float* __restrict__ scales,

@@ -123,7 +123,7 @@ def test_a_slot_that_dominates(torch, kind, normalize, T, E, k):
 
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("normalize", [0, 1])
-@pytest.mark.parametrize("E,k", [(6, 3), (70, 5), (200, 70), (1000, 300)])
+@pytest.mark.parametrize("E,k", [(6, 3), (70, 5), (200, 70), (1000, 300), (1024, 1024)])
 def test_any_indices(torch, kind, normalize, E, k):
     # repeated, masked and outside ones
     r = np.random.default_rng(E + k)
