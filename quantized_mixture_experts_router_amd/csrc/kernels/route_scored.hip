@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(256) qmoe_route_scored(const float* __restrict
 // or outside ones), S = sum u, g the slots' gradients and D_e the sum over the
 // slots of e:
 //   as they are:    sigmoid   gl_e = scale D_e s_e (1 - s_e)      softmax   gl_e = scale s_e (D_e - sum_i u_i g_i)
-//   renormalised:   with g_i - sum_i u_i g_i / S in the place of g_i and s_e / S in the place of the first s_e, where the
+//   renormalised:   with g_i - sum_j u_j g_j / S in the place of g_i and s_e / S in the place of the first s_e, where the
 //                   softmax's sum is 0 by itself (all 0 where S is)
 // The differences cancel: renormalised, one slot has a gradient of 0, and where one
 // holds nearly all of S (or of the softmax) what is left is far below the g's.  So
@@ -282,7 +282,9 @@ __global__ void __launch_bounds__(256) qmoe_route_scored_grad(const float* __res
   }
 #pragma unroll
   for (int j = 0; j < V; ++j) p[j] = v[j] == -INFINITY ? -1.0 : p[j];
-  double S = 0.0, dot = 0.0;
+  // (renormalised: the slots' gradients from the first held one's, so that a single slot leaves exactly 0)
+  double S = 0.0, dot = 0.0, g0 = 0.0;
+  bool first = a.normalize;
   for (int s0 = 0; s0 < a.k; s0 += 64) {  // (every lane stays: its scores are read)
     const int s = s0 + lane;
     const long at = (long)t * a.k + min(s, a.k - 1);
@@ -295,21 +297,26 @@ __global__ void __launch_bounds__(256) qmoe_route_scored_grad(const float* __res
       const double x = __shfl(p[j], i & 63);
       u = i >> 6 == j ? x : u;
     }
+    const bool on = s < a.k && u >= 0.0;
+    const unsigned long long all = __ballot(on);
+    if (first && all) {
+      g0 = (double)__shfl(g, __ffsll((long long)all) - 1);
+      first = false;
+    }
     if (s >= a.k) continue;
-    const bool on = u >= 0.0;
     u = on ? u : 0.0;
+    const double x = on ? (double)g - g0 : 0.0;
     se[s] = on ? i : -1;
-    sv[s] = on ? (double)g : 0.0;
+    sv[s] = x;
     S += u;
-    dot = fma(u, on ? (double)g : 0.0, dot);
+    dot = fma(u, x, dot);
   }
   S = wave_sum_double(S);
   dot = wave_sum_double(dot);
   double shift = 0.0, mean = dot, over = 1.0;
   if (a.normalize) {
-    // (a division: u g / u is g where one slot is left)
-    shift = S > 0.0 ? dot / S : 0.0;
     over = S > 0.0 ? reciprocal(S) : 0.0;
+    shift = dot * over;
     mean = 0.0;
   }
   // (one wavefront's own LDS words: written and read in program order)

@@ -84,6 +84,10 @@ def check(torch, l, idx, kind, normalize, scale, index_type="int32", seed=9):
                                    torch.from_numpy(np.ascontiguousarray(idx.astype(index_type))).cuda(),
                                    {"scores": kind, "normalize_routing_weights": normalize, "scale": scale})
     ref, mag = reference(g.astype(np.float64), l.astype(np.float64), idx, kind, normalize, scale)
+    if normalize:  # a row of one slot: nothing at all
+        off = scores_of(l.astype(np.float64), kind)[2]
+        one = [sum(0 <= e < l.shape[1] and not off[t, e] for e in idx[t]) == 1 for t in range(T)]
+        assert not got.cpu().numpy()[one].any()
     U.check(U.back(got), ref, 2.0 ** -24 * (1 + 2.0 ** -20) * np.abs(ref) + (k + 16) * 2.0 ** -44 * mag + 2.0 ** -149, "grad_logits")
 
 
